@@ -179,6 +179,74 @@ int jamba_moe_forward_fp8(const uint16_t* x, const float* router_W, const float*
                           int path);
 
 /*
+ * MX4: microscaled 4-bit operands (OCP Microscaling Formats v1.0, MXFP4).  32 consecutive elements of a
+ * row share one E8M0 scale 2^(s - 127), s a byte (255 = NaN); each element is an E2M1 number (1 sign, 2
+ * exponent bits with bias 1, 1 mantissa bit: +-{0, 0.5, 1, 1.5, 2, 3, 4, 6}).  Codes: uint8
+ * [...][cols / 2], element 2i in the low half of byte i; scales: uint8 [...][cols / 32].  The tensor
+ * cores of sm_100a multiply such operands as they are (tcgen05 kind::mxf4 with block scales), at four
+ * times their bf16 rate, and a weight takes 17/32 of an int8 code's bytes.  As in the FP8 layer, both operands of
+ * a product are in the format.
+ *
+ * jamba_moe_quantize_mx4 — W bf16 [n_mats][rows][cols] (weights or activations) to codes Q and scales
+ * S.  For each block with largest magnitude m > 0: scale = 2^(floor(log2 m) - 2), at least 2^-127;
+ * code = the E2M1 number nearest to the exact quotient, ties to the even code, saturating at +-6 (an
+ * element of 6 to 8 scales saturates: the format's rule).  A block of zeros gets s = 127; a block holding
+ * a NaN or an infinity gets s = 255 and codes 0, and makes every product it enters NaN.  A zero
+ * keeps its sign.  Bit-exact and deterministic.
+ * Sizes: n_mats, rows >= 1, cols % 32 == 0, 32 <= cols <= 1<<20, at most 2^40 elements; W, Q 16-byte, S 4-byte aligned.
+ *
+ * jamba_moe_dequantize_mx4 — the values of codes and scales as bf16 [n_mats][rows][cols], exact (every
+ * MX4 value within bf16's range is a bf16 number).  Sizes and alignment as in jamba_moe_quantize_mx4.
+ */
+int jamba_moe_quantize_mx4(const uint16_t* W, int64_t n_mats, int64_t rows, int64_t cols, uint8_t* Q, uint8_t* S,
+                           void* stream);
+int jamba_moe_dequantize_mx4(const uint8_t* Q, const uint8_t* S, int64_t n_mats, int64_t rows, int64_t cols,
+                             uint16_t* W, void* stream);
+
+/*
+ * jamba_moe_grouped_mx4 — matrix products grouped by expert, with ragged sizes: for the rows
+ * offsets[e] <= r < offsets[e + 1] of expert e,
+ *
+ *     y[r][i] = sum_k x^[r][k] * W^_e[i][k]          (v^: the value of an MX4 code times its scale)
+ *
+ *   xq, xs:  codes uint8 [N][cols / 2], scales uint8 [N][cols / 32] of the rows, grouped by expert
+ *   offsets: int32 [n_experts + 1], on the device, 0 <= offsets[0] <= ... <= offsets[n_experts] <= N.
+ *            An expert may have no row; its weights are then not read.  Offsets that break the rule are
+ *            reported as JMOE_DEV_BAD_INDEX in the workspace status word; no access leaves the
+ *            arrays, and y is then not valid.
+ *   Q, S:    codes uint8 [n_experts][rows][cols / 2], scales uint8 [n_experts][rows][cols / 32]
+ *   y:       [N][rows], bf16 (out_type JMOE_OUT_BF16) or fp32 (JMOE_OUT_FP32).  Rows that belong to no
+ *            expert are left as they were.
+ *   workspace: device scratch of at least jamba_moe_grouped_mx4_workspace_size(...) bytes, 256-byte
+ *            aligned, contents on entry irrelevant; not shared by overlapping calls.
+ *
+ * Numerics: products exact, accumulated in fp32, rounded once to the output type; deterministic.
+ * Sizes: 0 <= N <= 1<<20, 1 <= rows <= 65536, cols a multiple of 128 in [128, 32768], 1 <= n_experts <= 256
+ * (not only the layer's 16: any model's experts, or one dense matrix); xq, Q, y 16-byte, xs, S, offsets 4-byte
+ * aligned.  N = 0 returns at once.
+ */
+enum { JMOE_OUT_BF16 = 0, JMOE_OUT_FP32 = 1 };
+size_t jamba_moe_grouped_mx4_workspace_size(int64_t N, int64_t rows, int64_t cols, int n_experts);
+int jamba_moe_grouped_mx4(const uint8_t* xq, const uint8_t* xs, const int32_t* offsets, int64_t N, int64_t rows,
+                          int64_t cols, int n_experts, const uint8_t* Q, const uint8_t* S, void* y, int out_type,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * jamba_moe_forward_mx4 — the MoE layer on MX4 expert weights: arguments as jamba_moe_forward, with
+ * Q1, Q3 uint8 [n_experts][ffn][d / 2], S1, S3 uint8 [n_experts][ffn][d / 32], Q2 uint8
+ * [n_experts][d][ffn / 2], S2 uint8 [n_experts][d][ffn / 32] from jamba_moe_quantize_mx4 and a workspace of
+ * jamba_moe_workspace_size_mx4 bytes.  x is quantized per token; the SwiGLU output of the first products
+ * is rounded to bf16 and quantized per expert row; the grouped products are those of
+ * jamba_moe_grouped_mx4.  Router and combine as in jamba_moe_forward.  Deterministic; errors as
+ * jamba_moe_forward.
+ */
+size_t jamba_moe_workspace_size_mx4(int64_t T, int64_t d, int64_t ffn, int n_experts, int top_k);
+int jamba_moe_forward_mx4(const uint16_t* x, const float* router_W, const float* router_bias, const uint8_t* Q1,
+                          const uint8_t* S1, const uint8_t* Q3, const uint8_t* S3, const uint8_t* Q2,
+                          const uint8_t* S2, int64_t T, int64_t d, int64_t ffn, int n_experts, int top_k, uint16_t* y,
+                          int32_t* topk_ids, float* topk_w, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * jamba_mlp_workspace_size — bytes of device scratch jamba_mlp_forward needs for these sizes.
  * Returns 0 for unsupported sizes.  Host only; touches no device.
  */
@@ -362,7 +430,9 @@ enum {
     JMOE_KERNEL_GEMM2 = 7,
     JMOE_KERNEL_COMBINE = 8,
     JMOE_KERNEL_ACT_QUANT = 9, /* FP8 layer: per-row E4M3 quantization of x and of the intermediate h */
-    JMOE_KERNEL_KINDS = 10
+    JMOE_KERNEL_DEQUANTIZE = 10, /* MX4: codes and scales back to bf16 */
+    JMOE_KERNEL_GROUPED = 11,    /* MX4: jamba_moe_grouped_mx4 */
+    JMOE_KERNEL_KINDS = 12
 };
 int jamba_moe_timing_start(int max_launches);
 int jamba_moe_timing_collect(double* total_ms, int64_t* launches, int n_kinds);

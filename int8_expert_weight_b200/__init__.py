@@ -8,7 +8,9 @@ into a ``JmoeError``.  PyTorch provides device memory and streams; there is no C
 Functions keep the C names: ``jamba_moe_quantize``, ``jamba_moe_workspace_size``,
 ``jamba_moe_forward`` (the ExpertsInt8 MoE layer), ``jamba_moe_forward_bf16w`` (unquantized bf16
 weights), ``jamba_moe_quantize_fp8`` / ``jamba_moe_workspace_size_fp8`` / ``jamba_moe_forward_fp8``
-(the FP8 comparator layer), ``jamba_mlp_workspace_size`` / ``jamba_mlp_forward`` (the dense
+(the FP8 comparator layer), ``jamba_moe_quantize_mx4`` / ``jamba_moe_dequantize_mx4`` /
+``jamba_moe_grouped_mx4`` / ``jamba_moe_forward_mx4`` and their workspace sizes (microscaled 4-bit
+operands: quantization, the product grouped by expert, the layer), ``jamba_mlp_workspace_size`` / ``jamba_mlp_forward`` (the dense
 ExpertsInt8 MLP), ``jamba_moe_forward_noalloc``, ``jamba_moe_read_device_status``,
 ``jamba_moe_status_string``, ``jamba_moe_timing_start``, ``jamba_moe_timing_collect``.
 """
@@ -25,7 +27,8 @@ N_EXPERTS = 16
 TOP_K = 2
 PATH_AUTO, PATH_GEMV, PATH_GEMM = 0, 1, 2
 KERNEL_NAMES = ["quantize", "router", "permute", "gather", "gemv13", "gemv2", "gemm13", "gemm2", "combine",
-                "act_quant"]
+                "act_quant", "dequantize", "grouped"]
+OUT_BF16, OUT_FP32 = 0, 1
 
 
 class JmoeError(RuntimeError):
@@ -58,6 +61,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.jamba_moe_workspace_size_fp8.argtypes = [i64, i64, i64, c_int, c_int]
     lib.jamba_moe_forward_fp8.restype = c_int
     lib.jamba_moe_forward_fp8.argtypes = fwd_args + [c_int]
+    lib.jamba_moe_quantize_mx4.restype = c_int
+    lib.jamba_moe_quantize_mx4.argtypes = [vp, i64, i64, i64, vp, vp, vp]
+    lib.jamba_moe_dequantize_mx4.restype = c_int
+    lib.jamba_moe_dequantize_mx4.argtypes = [vp, vp, i64, i64, i64, vp, vp]
+    lib.jamba_moe_grouped_mx4_workspace_size.restype = sz
+    lib.jamba_moe_grouped_mx4_workspace_size.argtypes = [i64, i64, i64, c_int]
+    lib.jamba_moe_grouped_mx4.restype = c_int
+    lib.jamba_moe_grouped_mx4.argtypes = [vp, vp, vp, i64, i64, i64, c_int, vp, vp, vp, c_int, vp, sz, vp]
+    lib.jamba_moe_workspace_size_mx4.restype = sz
+    lib.jamba_moe_workspace_size_mx4.argtypes = [i64, i64, i64, c_int, c_int]
+    lib.jamba_moe_forward_mx4.restype = c_int
+    lib.jamba_moe_forward_mx4.argtypes = fwd_args
     lib.jamba_mlp_workspace_size.restype = sz
     lib.jamba_mlp_workspace_size.argtypes = [i64, i64, i64]
     mlp_args = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, vp, vp, sz, vp]
@@ -316,6 +331,161 @@ def jamba_moe_forward_fp8(x: torch.Tensor, router_W: torch.Tensor, router_bias: 
                                        workspace.numel(), _stream_ptr(stream, dev), int(path))
     if st != 0:
         raise JmoeError(st, "jamba_moe_forward_fp8")
+    return y, topk_ids, topk_w
+
+
+def jamba_moe_quantize_mx4(W: torch.Tensor, stream: Optional[torch.cuda.Stream] = None,
+                           out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """MX4 quantization of bf16 rows [..., rows, cols], cols a multiple of 32 (weights or activations).
+    Returns (Q uint8 [..., rows, cols / 2], two E2M1 codes a byte, the even element low;
+    S uint8 [..., rows, cols / 32], one E8M0 scale per block of 32)."""
+    lib = load_library()
+    _check(W, "W", torch.bfloat16)
+    if W.dim() < 2:
+        raise ValueError("W must have at least 2 dims (rows, cols)")
+    rows, cols = W.shape[-2], W.shape[-1]
+    n_mats = W.numel() // (rows * cols) if W.numel() else 0
+    q_shape, s_shape = W.shape[:-1] + (cols // 2,), W.shape[:-1] + (cols // 32,)
+    if out is None:
+        Q = torch.empty(q_shape, dtype=torch.uint8, device=W.device)
+        S = torch.empty(s_shape, dtype=torch.uint8, device=W.device)
+    else:
+        Q, S = out
+        _check(Q, "Q", torch.uint8, q_shape)
+        _check(S, "S", torch.uint8, s_shape)
+    dev = _one_device(W, Q=Q, S=S)
+    with torch.cuda.device(dev):
+        st = lib.jamba_moe_quantize_mx4(W.data_ptr(), n_mats, rows, cols, Q.data_ptr(), S.data_ptr(),
+                                        _stream_ptr(stream, dev))
+    if st != 0:
+        raise JmoeError(st, "jamba_moe_quantize_mx4")
+    return Q, S
+
+
+def jamba_moe_dequantize_mx4(Q: torch.Tensor, S: torch.Tensor, out: Optional[torch.Tensor] = None,
+                             stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The values of MX4 codes Q uint8 [..., rows, cols / 2] and scales S uint8 [..., rows, cols / 32]
+    as bf16 [..., rows, cols], exact."""
+    lib = load_library()
+    _check(Q, "Q", torch.uint8)
+    if Q.dim() < 2:
+        raise ValueError("Q must have at least 2 dims (rows, cols / 2)")
+    rows, cols = Q.shape[-2], 2 * Q.shape[-1]
+    _check(S, "S", torch.uint8, Q.shape[:-1] + (cols // 32,))
+    n_mats = Q.numel() // (rows * (cols // 2)) if Q.numel() else 0
+    w_shape = Q.shape[:-1] + (cols,)
+    if out is None:
+        out = torch.empty(w_shape, dtype=torch.bfloat16, device=Q.device)
+    _check(out, "out", torch.bfloat16, w_shape)
+    dev = _one_device(Q, S=S, out=out)
+    with torch.cuda.device(dev):
+        st = lib.jamba_moe_dequantize_mx4(Q.data_ptr(), S.data_ptr(), n_mats, rows, cols, out.data_ptr(),
+                                          _stream_ptr(stream, dev))
+    if st != 0:
+        raise JmoeError(st, "jamba_moe_dequantize_mx4")
+    return out
+
+
+def jamba_moe_grouped_mx4_workspace_size(N: int, rows: int, cols: int, n_experts: int) -> int:
+    return int(load_library().jamba_moe_grouped_mx4_workspace_size(N, rows, cols, n_experts))
+
+
+def jamba_moe_grouped_mx4(xq: torch.Tensor, xs: torch.Tensor, offsets: torch.Tensor, Q: torch.Tensor, S: torch.Tensor,
+                          out_dtype: torch.dtype = torch.bfloat16, y: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None,
+                          stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Products grouped by expert on MX4 operands (from jamba_moe_quantize_mx4): rows offsets[e] to
+    offsets[e + 1] of x (codes xq uint8 [N][cols / 2], scales xs uint8 [N][cols / 32]) with the weights of
+    expert e (codes Q uint8 [n_experts][rows][cols / 2], scales S uint8 [n_experts][rows][cols / 32]);
+    offsets int32 [n_experts + 1] on the device.  Returns y [N][rows] in out_dtype (torch.bfloat16 or
+    torch.float32); rows that belong to no expert are left as they were (unset if y is not given).
+    ``workspace`` (uint8, >= jamba_moe_grouped_mx4_workspace_size bytes) is allocated when not given."""
+    lib = load_library()
+    _check(xq, "xq", torch.uint8)
+    _check(Q, "Q", torch.uint8)
+    if xq.dim() != 2 or Q.dim() != 3:
+        raise ValueError("xq must be [N][cols / 2], Q [n_experts][rows][cols / 2]")
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
+    N, cols = xq.shape[0], 2 * xq.shape[1]
+    E, rows = Q.shape[0], Q.shape[1]
+    _check(Q, "Q", torch.uint8, (E, rows, cols // 2))
+    _check(xs, "xs", torch.uint8, (N, cols // 32))
+    _check(S, "S", torch.uint8, (E, rows, cols // 32))
+    _check(offsets, "offsets", torch.int32, (E + 1,))
+    if y is None:
+        y = torch.empty((N, rows), dtype=out_dtype, device=xq.device)
+    _check(y, "y", out_dtype, (N, rows))
+    need = jamba_moe_grouped_mx4_workspace_size(N, rows, cols, E)
+    if need == 0:
+        raise JmoeError(2, "jamba_moe_grouped_mx4_workspace_size")
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=xq.device)
+    _check(workspace, "workspace", torch.uint8)
+    dev = _one_device(xq, xs=xs, offsets=offsets, Q=Q, S=S, y=y, workspace=workspace)
+    with torch.cuda.device(dev):
+        st = lib.jamba_moe_grouped_mx4(xq.data_ptr(), xs.data_ptr(), offsets.data_ptr(), N, rows, cols, E,
+                                       Q.data_ptr(), S.data_ptr(), y.data_ptr(),
+                                       OUT_BF16 if out_dtype == torch.bfloat16 else OUT_FP32, workspace.data_ptr(),
+                                       workspace.numel(), _stream_ptr(stream, dev))
+    if st != 0:
+        raise JmoeError(st, "jamba_moe_grouped_mx4")
+    return y
+
+
+def jamba_moe_workspace_size_mx4(T: int, d: int, ffn: int, n_experts: int = N_EXPERTS, top_k: int = TOP_K) -> int:
+    return int(load_library().jamba_moe_workspace_size_mx4(T, d, ffn, n_experts, top_k))
+
+
+def jamba_moe_forward_mx4(x: torch.Tensor, router_W: torch.Tensor, router_bias: Optional[torch.Tensor],
+                          Q1: torch.Tensor, S1: torch.Tensor, Q3: torch.Tensor, S3: torch.Tensor,
+                          Q2: torch.Tensor, S2: torch.Tensor, y: Optional[torch.Tensor] = None,
+                          topk_ids: Optional[torch.Tensor] = None, topk_w: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """The MoE layer on MX4 expert weights: as jamba_moe_forward with Q1, Q3 uint8 [16][ffn][d / 2],
+    S1, S3 uint8 [16][ffn][d / 32], Q2 uint8 [16][d][ffn / 2], S2 uint8 [16][d][ffn / 32] from
+    jamba_moe_quantize_mx4.  Returns (y, topk_ids, topk_w)."""
+    lib = load_library()
+    _check(x, "x", torch.bfloat16)
+    if x.dim() != 2:
+        raise ValueError("x must be [T][d]")
+    T, d = x.shape
+    E = router_W.shape[0]
+    ffn = Q1.shape[1]
+    _check(router_W, "router_W", torch.float32, (E, d))
+    if router_bias is not None:
+        _check(router_bias, "router_bias", torch.float32, (E,))
+    _check(Q1, "Q1", torch.uint8, (E, ffn, d // 2))
+    _check(Q3, "Q3", torch.uint8, (E, ffn, d // 2))
+    _check(Q2, "Q2", torch.uint8, (E, d, ffn // 2))
+    _check(S1, "S1", torch.uint8, (E, ffn, d // 32))
+    _check(S3, "S3", torch.uint8, (E, ffn, d // 32))
+    _check(S2, "S2", torch.uint8, (E, d, ffn // 32))
+    if y is None:
+        y = torch.empty((T, d), dtype=torch.bfloat16, device=x.device)
+    _check(y, "y", torch.bfloat16, (T, d))
+    if topk_ids is None:
+        topk_ids = torch.empty((T, TOP_K), dtype=torch.int32, device=x.device)
+    if topk_w is None:
+        topk_w = torch.empty((T, TOP_K), dtype=torch.float32, device=x.device)
+    _check(topk_ids, "topk_ids", torch.int32, (T, TOP_K))
+    _check(topk_w, "topk_w", torch.float32, (T, TOP_K))
+    need = jamba_moe_workspace_size_mx4(T, d, ffn, E, TOP_K)
+    if need == 0:
+        raise JmoeError(2, "jamba_moe_workspace_size_mx4")
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    _check(workspace, "workspace", torch.uint8)
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    dev = _one_device(x, router_W=router_W, router_bias=router_bias, Q1=Q1, S1=S1, Q3=Q3, S3=S3, Q2=Q2, S2=S2, y=y,
+                      topk_ids=topk_ids, topk_w=topk_w, workspace=workspace)
+    with torch.cuda.device(dev):
+        st = lib.jamba_moe_forward_mx4(x.data_ptr(), router_W.data_ptr(), p(router_bias), Q1.data_ptr(),
+                                       S1.data_ptr(), Q3.data_ptr(), S3.data_ptr(), Q2.data_ptr(), S2.data_ptr(), T, d,
+                                       ffn, E, TOP_K, y.data_ptr(), p(topk_ids), p(topk_w), workspace.data_ptr(),
+                                       workspace.numel(), _stream_ptr(stream, dev))
+    if st != 0:
+        raise JmoeError(st, "jamba_moe_forward_mx4")
     return y, topk_ids, topk_w
 
 

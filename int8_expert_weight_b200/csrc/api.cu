@@ -4,6 +4,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "mx4.cuh"
 
 namespace jmoe {
 
@@ -60,6 +61,14 @@ cudaError_t launch_gemm13_f8(WsHeader* hdr, const int32_t* perm, const uint8_t* 
 cudaError_t launch_gemm2_f8(WsHeader* hdr, const int32_t* perm, const uint8_t* h8, const float* sh, const uint8_t* Q2,
                             const float* S2, const float* wts, float* out_slot, int64_t rows_cap, int64_t d, int64_t F,
                             cudaStream_t st);
+
+cudaError_t launch_quantize_mx4(const uint16_t* W, int64_t elements, uint8_t* Q, uint8_t* S, cudaStream_t st,
+                                int num_sms);
+cudaError_t launch_quantize_mx4_rows(const uint16_t* x, const int32_t* perm, const int32_t* n_live, int64_t cap_rows,
+                                     int64_t cols, int k_div, uint8_t* Q, uint8_t* S, cudaStream_t st, int num_sms);
+cudaError_t launch_dequantize_mx4(const uint8_t* Q, const uint8_t* S, int64_t elements, uint16_t* W, cudaStream_t st,
+                                  int num_sms);
+cudaError_t launch_grouped_mx4(const mx4::Args& p, cudaStream_t st);
 
 cudaError_t launch_tables_check(WsHeader* hdr, const int32_t* ids, const int32_t* perm, const int32_t* inv, int64_t TK,
                                 int64_t rows_cap, cudaStream_t st);
@@ -704,7 +713,8 @@ int jamba_moe_timing_collect(double* total_ms, int64_t* launches, int n_kinds) {
 
 const char* jamba_moe_kernel_name(int kind) {
     static const char* names[JMOE_KERNEL_KINDS] = {"quantize", "router", "permute", "gather", "gemv13",
-                                                   "gemv2", "gemm13", "gemm2", "combine", "act_quant"};
+                                                   "gemv2", "gemm13", "gemm2", "combine", "act_quant",
+                                                   "dequantize", "grouped"};
     return (kind >= 0 && kind < JMOE_KERNEL_KINDS) ? names[kind] : "unknown";
 }
 
@@ -874,6 +884,225 @@ int jamba_moe_ep_combine(const float* ret, const int32_t* pos, int64_t T, int64_
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     TimedLaunch t(JMOE_KERNEL_COMBINE, st);
     return to_status(launch_ep_combine(ret, pos, T, d, y, st, num_sms_current()));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- MX4: microscaled 4-bit operands
+namespace {
+
+constexpr int64_t kMaxRowsMx4 = 65536;
+
+bool rows_ok_mx4(int64_t n_mats, int64_t rows, int64_t cols) {
+    return n_mats >= 1 && rows >= 1 && cols >= 32 && cols <= (int64_t(1) << 20) && cols % 32 == 0 &&
+           n_mats <= (int64_t(1) << 40) / cols / rows;
+}
+
+bool grouped_shape_ok(int64_t N, int64_t rows, int64_t cols, int E) {
+    return N >= 0 && N <= kMaxT && rows >= 1 && rows <= kMaxRowsMx4 && cols >= 128 && cols <= kMaxDim &&
+           cols % 128 == 0 && E >= 1 && E <= mx4::kMaxGroups;
+}
+
+struct LayoutMx4 {
+    int64_t rows_cap;
+    size_t hdr, ids, wts, inv, perm, xq, xs, h, hq, hs, slots, total;
+    GuardGaps guards;
+};
+
+LayoutMx4 make_layout_mx4(int64_t T, int64_t d, int64_t F) {
+    LayoutMx4 L{};
+    const int64_t TK = T * kTopK;
+    L.rows_cap = (TK + int64_t(kExperts) * (kRowPad - 1) + kRowPad - 1) / kRowPad * kRowPad;
+    Regions R;
+    L.hdr = R.take(kHeaderBytes);
+    L.ids = R.take(sizeof(int32_t) * TK);
+    L.wts = R.take(sizeof(float) * TK);
+    L.inv = R.take(sizeof(int32_t) * TK);
+    L.perm = R.take(sizeof(int32_t) * L.rows_cap);
+    L.xq = R.take((size_t)L.rows_cap * (d / 2));
+    L.xs = R.take((size_t)L.rows_cap * (d / 32));
+    L.h = R.take(sizeof(uint16_t) * L.rows_cap * F);
+    L.hq = R.take((size_t)L.rows_cap * (F / 2));
+    L.hs = R.take((size_t)L.rows_cap * (F / 32));
+    L.slots = R.take(sizeof(float) * TK * d);
+    L.total = R.off;
+    L.guards = R.g;
+    return L;
+}
+
+}  // namespace
+
+extern "C" {
+
+int jamba_moe_quantize_mx4(const uint16_t* W, int64_t n_mats, int64_t rows, int64_t cols, uint8_t* Q, uint8_t* S,
+                           void* stream) {
+    if (!W || !Q || !S) return JMOE_ERR_NULL;
+    if (!rows_ok_mx4(n_mats, rows, cols)) return JMOE_ERR_SHAPE;
+    if (!aligned16(W) || !aligned16(Q) || (reinterpret_cast<uintptr_t>(S) & 3)) return JMOE_ERR_ALIGN;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    TimedLaunch t(JMOE_KERNEL_QUANTIZE, st);
+    return to_status(launch_quantize_mx4(W, n_mats * rows * cols, Q, S, st, num_sms_current()));
+}
+
+int jamba_moe_dequantize_mx4(const uint8_t* Q, const uint8_t* S, int64_t n_mats, int64_t rows, int64_t cols,
+                             uint16_t* W, void* stream) {
+    if (!W || !Q || !S) return JMOE_ERR_NULL;
+    if (!rows_ok_mx4(n_mats, rows, cols)) return JMOE_ERR_SHAPE;
+    if (!aligned16(W) || !aligned16(Q) || (reinterpret_cast<uintptr_t>(S) & 3)) return JMOE_ERR_ALIGN;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    TimedLaunch t(JMOE_KERNEL_DEQUANTIZE, st);
+    return to_status(launch_dequantize_mx4(Q, S, n_mats * rows * cols, W, st, num_sms_current()));
+}
+
+size_t jamba_moe_grouped_mx4_workspace_size(int64_t N, int64_t rows, int64_t cols, int n_experts) {
+    if (!grouped_shape_ok(N, rows, cols, n_experts)) return 0;
+    return kHeaderBytes;
+}
+
+int jamba_moe_grouped_mx4(const uint8_t* xq, const uint8_t* xs, const int32_t* offsets, int64_t N, int64_t rows,
+                          int64_t cols, int n_experts, const uint8_t* Q, const uint8_t* S, void* y, int out_type,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+    if (!grouped_shape_ok(N, rows, cols, n_experts)) return JMOE_ERR_SHAPE;
+    if (out_type != JMOE_OUT_BF16 && out_type != JMOE_OUT_FP32) return JMOE_ERR_SHAPE;
+    if (N == 0) return JMOE_OK;
+    if (!xq || !xs || !offsets || !Q || !S || !y || !workspace) return JMOE_ERR_NULL;
+    const void* ptrs16[] = {xq, Q, y};
+    for (const void* p : ptrs16)
+        if (!aligned16(p)) return JMOE_ERR_ALIGN;
+    const void* ptrs4[] = {xs, S, offsets};
+    for (const void* p : ptrs4)
+        if (reinterpret_cast<uintptr_t>(p) & 3) return JMOE_ERR_ALIGN;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255) return JMOE_ERR_WORKSPACE;
+    if (workspace_bytes < jamba_moe_grouped_mx4_workspace_size(N, rows, cols, n_experts)) return JMOE_ERR_WORKSPACE;
+    mx4::Args p{};
+    p.hdr = static_cast<WsHeader*>(workspace);
+    p.begin = offsets;
+    p.E = n_experts;
+    p.reset_status = 1;
+    p.N = N;
+    p.xq = xq;
+    p.xs = xs;
+    p.qa = Q;
+    p.sa = S;
+    if (out_type == JMOE_OUT_BF16)
+        p.y16 = static_cast<uint16_t*>(y);
+    else
+        p.y32 = static_cast<float*>(y);
+    p.K = (int)cols;
+    p.M = (int)rows;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    TimedLaunch t(JMOE_KERNEL_GROUPED, st);
+    return to_status(launch_grouped_mx4(p, st));
+}
+
+size_t jamba_moe_workspace_size_mx4(int64_t T, int64_t d, int64_t ffn, int n_experts, int top_k) {
+    if (!shape_ok(T, d, ffn, n_experts, top_k)) return 0;
+    return make_layout_mx4(T, d, ffn).total;
+}
+
+int jamba_moe_forward_mx4(const uint16_t* x, const float* router_W, const float* router_bias, const uint8_t* Q1,
+                          const uint8_t* S1, const uint8_t* Q3, const uint8_t* S3, const uint8_t* Q2,
+                          const uint8_t* S2, int64_t T, int64_t d, int64_t ffn, int n_experts, int top_k, uint16_t* y,
+                          int32_t* topk_ids, float* topk_w, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!shape_ok(T, d, ffn, n_experts, top_k)) return JMOE_ERR_SHAPE;
+    if (T == 0) return JMOE_OK;
+    if (!x || !router_W || !Q1 || !S1 || !Q3 || !S3 || !Q2 || !S2 || !y || !workspace) return JMOE_ERR_NULL;
+    const void* ptrs16[] = {x, Q1, Q3, Q2, y, router_W};
+    for (const void* p : ptrs16)
+        if (!aligned16(p)) return JMOE_ERR_ALIGN;
+    const void* ptrs4[] = {router_bias, S1, S3, S2, topk_ids, topk_w};
+    for (const void* p : ptrs4)
+        if (reinterpret_cast<uintptr_t>(p) & 3) return JMOE_ERR_ALIGN;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255) return JMOE_ERR_WORKSPACE;
+    const LayoutMx4 L = make_layout_mx4(T, d, ffn);
+    if (workspace_bytes < L.total) return JMOE_ERR_WORKSPACE;
+
+    char* ws = static_cast<char*>(workspace);
+    WsHeader* hdr = reinterpret_cast<WsHeader*>(ws + L.hdr);
+    int32_t* ids = reinterpret_cast<int32_t*>(ws + L.ids);
+    float* wts = reinterpret_cast<float*>(ws + L.wts);
+    int32_t* inv = reinterpret_cast<int32_t*>(ws + L.inv);
+    int32_t* perm = reinterpret_cast<int32_t*>(ws + L.perm);
+    uint8_t* xq = reinterpret_cast<uint8_t*>(ws + L.xq);
+    uint8_t* xs = reinterpret_cast<uint8_t*>(ws + L.xs);
+    uint16_t* h = reinterpret_cast<uint16_t*>(ws + L.h);
+    uint8_t* hq = reinterpret_cast<uint8_t*>(ws + L.hq);
+    uint8_t* hs = reinterpret_cast<uint8_t*>(ws + L.hs);
+    float* slots = reinterpret_cast<float*>(ws + L.slots);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int sms = num_sms_current();
+
+    const int64_t TK = T * kTopK;
+    cudaError_t e = debug_step(kAtStart, ws, L.guards, hdr, ids, perm, inv, TK, L.rows_cap, st);
+    if (e != cudaSuccess) return JMOE_ERR_CUDA;
+    {
+        TimedLaunch t(JMOE_KERNEL_ROUTER, st);
+        e = launch_router(x, router_W, router_bias, T, d, ids, wts, topk_ids, topk_w, st);
+    }
+    if (e != cudaSuccess) return JMOE_ERR_CUDA;
+    if (debug_step(kAfterRouter, ws, L.guards, hdr, ids, perm, inv, TK, L.rows_cap, st) != cudaSuccess)
+        return JMOE_ERR_CUDA;
+    {
+        TimedLaunch t(JMOE_KERNEL_PERMUTE, st);
+        e = launch_permute(ids, T, hdr, perm, inv, st);
+    }
+    if (e != cudaSuccess) return JMOE_ERR_CUDA;
+    if (debug_step(kAfterPermute, ws, L.guards, hdr, ids, perm, inv, TK, L.rows_cap, st) != cudaSuccess)
+        return JMOE_ERR_CUDA;
+    const int32_t* n_rows = &hdr->seg_start[kExperts];
+    {
+        TimedLaunch t(JMOE_KERNEL_ACT_QUANT, st);  // x rows in permuted order
+        e = launch_quantize_mx4_rows(x, perm, n_rows, L.rows_cap, d, kTopK, xq, xs, st, sms);
+    }
+    if (e != cudaSuccess) return JMOE_ERR_CUDA;
+    mx4::Args p{};
+    p.hdr = hdr;
+    p.begin = hdr->seg_start;
+    p.count = hdr->counts;
+    p.E = kExperts;
+    p.N = L.rows_cap;
+    p.xq = xq;
+    p.xs = xs;
+    p.qa = Q1;
+    p.sa = S1;
+    p.qb = Q3;
+    p.sb = S3;
+    p.y16 = h;
+    p.K = (int)d;
+    p.M = (int)ffn;
+    {
+        TimedLaunch t(JMOE_KERNEL_GEMM13, st);
+        e = launch_grouped_mx4(p, st);
+    }
+    if (e != cudaSuccess) return JMOE_ERR_CUDA;
+    {
+        TimedLaunch t(JMOE_KERNEL_ACT_QUANT, st);
+        e = launch_quantize_mx4_rows(h, perm, n_rows, L.rows_cap, ffn, 0, hq, hs, st, sms);
+    }
+    if (e != cudaSuccess) return JMOE_ERR_CUDA;
+    p.xq = hq;
+    p.xs = hs;
+    p.qa = Q2;
+    p.sa = S2;
+    p.qb = nullptr;
+    p.sb = nullptr;
+    p.perm = perm;
+    p.wts = wts;
+    p.y16 = nullptr;
+    p.y32 = slots;
+    p.K = (int)ffn;
+    p.M = (int)d;
+    {
+        TimedLaunch t(JMOE_KERNEL_GEMM2, st);
+        e = launch_grouped_mx4(p, st);
+    }
+    if (e != cudaSuccess) return JMOE_ERR_CUDA;
+    {
+        TimedLaunch t(JMOE_KERNEL_COMBINE, st);
+        e = launch_combine(slots, T, d, y, st, sms);
+    }
+    if (e != cudaSuccess) return JMOE_ERR_CUDA;
+    return to_status(debug_step(kAtEnd, ws, L.guards, hdr, ids, perm, inv, TK, L.rows_cap, st));
 }
 
 }  // extern "C"

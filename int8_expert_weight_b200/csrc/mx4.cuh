@@ -1,0 +1,48 @@
+// Arguments and group table of the MX4 products grouped by expert.
+#pragma once
+
+#include "common.cuh"
+
+namespace jmoe {
+namespace mx4 {
+
+constexpr int kMaxGroups = 256;
+
+struct Args {
+    WsHeader* hdr;         // device status word
+    const int32_t* begin;  // first row of each expert
+    const int32_t* count;  // rows of each expert, or NULL: begin has E + 1 entries and expert e ends at begin[e + 1]
+    int E;                 // experts
+    int reset_status;      // this call owns the status word: clear it, and report a bad group table there
+    int64_t N;             // rows of x
+    const uint8_t* xq;     // x codes [N][K / 2] and scales [N][K / 32]
+    const uint8_t* xs;
+    const uint8_t* qa;     // weights W (dual: W1) codes [E][M][K / 2] and scales [E][M][K / 32]
+    const uint8_t* sa;
+    const uint8_t* qb;     // dual: W3, else NULL
+    const uint8_t* sb;
+    const int32_t* perm;   // slot: assignment of each row, -1 = padding
+    const float* wts;      // slot: routing weight of each assignment, else NULL
+    uint16_t* y16;         // plain: y in bf16; dual: h
+    float* y32;            // plain: y in fp32; slot: out [T*K][M]
+    int K;                 // reduction length
+    int M;                 // weight rows per expert and matrix
+};
+
+// Rows of expert e.  Whatever the table holds, [row0, row0 + count) lies inside the N rows of x and y.
+__device__ __forceinline__ void group_at(const Args& p, int e, int64_t& row0, int& count) {
+    const int64_t b = p.begin[e];
+    const int64_t c = p.count ? p.count[e] : p.begin[e + 1] - b;
+    row0 = b < 0 ? 0 : (b > p.N ? p.N : b);
+    count = (int)(c < 0 ? 0 : (c > p.N - row0 ? p.N - row0 : c));
+}
+
+// Status of a caller's offsets: 0 <= begin[0] <= ... <= begin[E] <= N, or JMOE_DEV_BAD_INDEX.  By one thread.
+__device__ __forceinline__ void check_groups(const Args& p) {
+    bool bad = p.begin[0] < 0 || p.begin[p.E] > p.N;
+    for (int e = 0; e < p.E; ++e) bad |= p.begin[e] > p.begin[e + 1];
+    p.hdr->status = bad ? JMOE_DEV_BAD_INDEX : JMOE_OK;
+}
+
+}  // namespace mx4
+}  // namespace jmoe

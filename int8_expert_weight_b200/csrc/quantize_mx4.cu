@@ -1,0 +1,187 @@
+// MX4 quantization and its inverse (OCP Microscaling Formats v1.0, MXFP4): 32 consecutive elements of
+// a row share one E8M0 scale 2^(s - 127), each element is an E2M1 number (1 sign, 2 exponent bits with
+// bias 1, 1 mantissa bit: +-{0, 0.5, 1, 1.5, 2, 3, 4, 6}), two codes to a byte, the even element low.
+//
+// The scale of a block with largest magnitude m > 0 is 2^(floor(log2 m) - 2), so that m / scale lies
+// in [4, 8) and 4, the lower end of E2M1's last binade, is reached by every block; on bf16 bits that
+// is s = max(E - 2, 0) with E the exponent field of m (subnormal m: E = 0; 2^-127 is the least
+// E8M0 scale).  A block of zeros gets s = 127 (scale 1); a block holding a NaN or an infinity gets
+// s = 255 (E8M0's NaN) and codes 0.  v / scale is a multiplication by a power of two, exact in fp32
+// (the result is at most 8 in magnitude, and what falls below 2^-126 rounds to code 0 either way),
+// so the hardware's conversion (nearest, ties to even, saturating at +-6) of that product is the
+// correctly rounded code: no residual check as for the int8 and E4M3 codes is needed.
+//
+// HBM-bound: 2 bytes read and 17/32 written per element (and the reverse).  Blocks never straddle
+// rows (cols is a multiple of 32), so both kernels walk the matrices as one flat run of 8-element
+// chunks: a thread reads 16 bytes, four neighbouring lanes hold a block.
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace jmoe {
+
+constexpr int kMxThreads = 256;
+constexpr int kMxUnroll = 4;  // chunks a thread has in flight
+
+// Largest magnitude (bf16 bits) of the 8 values of a chunk.
+__device__ __forceinline__ uint32_t chunk_amax(const uint4& v) {
+    const uint32_t m2 = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                 __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+    return max(m2 & 0xFFFFu, m2 >> 16);
+}
+
+// E8M0 scale byte of a block from its largest magnitude (bf16 bits).
+__device__ __forceinline__ uint32_t mx_scale(uint32_t amax) {
+    if (amax >= 0x7F80u) return 255u;
+    if (amax == 0) return 127u;
+    return (uint32_t)max((int)(amax >> 7) - 2, 0);
+}
+
+// Codes of the 8 values of a chunk, element i in bits 4i .. 4i+3.
+__device__ __forceinline__ uint32_t mx_codes(const uint4& v, uint32_t s) {
+    if (s == 255u) return 0u;
+    const float r = __uint_as_float((254u - s) << 23);  // 1 / scale = 2^(127 - s)
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16) * r;
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u) * r;
+    }
+    uint32_t out;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(out)
+        : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+    return out;
+}
+
+// The block's largest magnitude across the four lanes that hold it.
+__device__ __forceinline__ uint32_t block_amax(uint32_t a) {
+    a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    return max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+}
+
+__global__ void __launch_bounds__(kMxThreads) quantize_mx4_kernel(const uint16_t* __restrict__ W, int64_t chunks,
+                                                                  uint8_t* __restrict__ Q, uint8_t* __restrict__ S) {
+    pdl_wait();
+    pdl_trigger();
+    const int64_t step = (int64_t)gridDim.x * kMxThreads;
+    // every lane of a warp takes part in the shuffles; chunks is a multiple of 4, so whole blocks are live
+    for (int64_t c0 = (int64_t)blockIdx.x * kMxThreads; c0 < chunks; c0 += kMxUnroll * step) {
+        uint4 v[kMxUnroll];
+#pragma unroll
+        for (int u = 0; u < kMxUnroll; ++u) {
+            const int64_t c = c0 + u * step + threadIdx.x;
+            v[u] = c < chunks ? ld_stream_v4(W + c * 8) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < kMxUnroll; ++u) {
+            const int64_t c = c0 + u * step + threadIdx.x;
+            const uint32_t s = mx_scale(block_amax(chunk_amax(v[u])));
+            if (c >= chunks) continue;
+            *reinterpret_cast<uint32_t*>(Q + c * 4) = mx_codes(v[u], s);
+            if ((c & 3) == 0) S[c >> 2] = (uint8_t)s;
+        }
+    }
+}
+
+// Rows of the layer: permuted row r takes x row perm[r] / k_div (k_div = 0: row r itself); rows whose
+// entry is -1 (padding) and rows from *n_live on are skipped.  One CTA per row.
+__global__ void __launch_bounds__(kMxThreads)
+    quantize_mx4_rows_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ perm,
+                             const int32_t* __restrict__ n_live, int64_t cap_rows, int cols, int k_div,
+                             uint8_t* __restrict__ Q, uint8_t* __restrict__ S) {
+    pdl_wait();
+    pdl_trigger();
+    const int64_t rows = min((int64_t)*n_live, cap_rows);
+    const int chunks = cols / 8;
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const int32_t a = perm[r];
+        if (a < 0) continue;
+        const uint16_t* xr = x + (k_div ? (int64_t)(a / k_div) : r) * cols;
+        uint8_t* qr = Q + r * (cols / 2);
+        uint8_t* sr = S + r * (cols / 32);
+        for (int c0 = 0; c0 < chunks; c0 += kMxThreads) {
+            const int c = c0 + threadIdx.x;
+            const uint4 v = c < chunks ? ld_nc_v4(xr + (int64_t)c * 8) : make_uint4(0, 0, 0, 0);
+            const uint32_t s = mx_scale(block_amax(chunk_amax(v)));
+            if (c >= chunks) continue;
+            *reinterpret_cast<uint32_t*>(qr + c * 4) = mx_codes(v, s);
+            if ((c & 3) == 0) sr[c >> 2] = (uint8_t)s;
+        }
+    }
+}
+
+// The inverse: code x scale as bf16, exact (an E2M1 number has two significant bits, and the least
+// magnitude, 2^-128, is a bf16 subnormal); products beyond bf16's range become infinities, a scale byte of 255 NaN.
+__global__ void __launch_bounds__(kMxThreads) dequantize_mx4_kernel(const uint8_t* __restrict__ Q,
+                                                                    const uint8_t* __restrict__ S, int64_t chunks,
+                                                                    uint16_t* __restrict__ W) {
+    pdl_wait();
+    pdl_trigger();
+    const int64_t step = (int64_t)gridDim.x * kMxThreads;
+    for (int64_t c0 = (int64_t)blockIdx.x * kMxThreads + threadIdx.x; c0 < chunks; c0 += kMxUnroll * step) {
+        uint32_t q[kMxUnroll], s[kMxUnroll];
+#pragma unroll
+        for (int u = 0; u < kMxUnroll; ++u) {
+            const int64_t c = c0 + u * step;
+            q[u] = c < chunks ? *reinterpret_cast<const uint32_t*>(Q + c * 4) : 0u;
+            s[u] = c < chunks ? S[c >> 2] : 127u;
+        }
+#pragma unroll
+        for (int u = 0; u < kMxUnroll; ++u) {
+            const int64_t c = c0 + u * step;
+            if (c >= chunks) continue;
+            const float sc = s[u] == 255u ? __uint_as_float(0x7FC00000u)
+                                          : __uint_as_float(s[u] == 0 ? 0x00400000u : s[u] << 23);
+            uint32_t h[4], o[4];
+            asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+                "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+                "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+                "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+                "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+                "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+                : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+                : "r"(q[u]));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+                o[i] = (uint32_t)f32_to_bf16_bits(f.x * sc) | ((uint32_t)f32_to_bf16_bits(f.y * sc) << 16);
+            }
+            *reinterpret_cast<uint4*>(W + c * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+}
+
+static unsigned mx_blocks(int64_t chunks, int num_sms) {
+    int64_t blocks = (chunks + kMxThreads - 1) / kMxThreads;
+    const int64_t cap = (int64_t)num_sms * 8;
+    return (unsigned)(blocks > cap ? cap : (blocks < 1 ? 1 : blocks));
+}
+
+// elements % 32 == 0.
+cudaError_t launch_quantize_mx4(const uint16_t* W, int64_t elements, uint8_t* Q, uint8_t* S, cudaStream_t st,
+                                int num_sms) {
+    return launch_pdl(quantize_mx4_kernel, dim3(mx_blocks(elements / 8, num_sms)), dim3(kMxThreads), 0, st, W,
+                      elements / 8, Q, S);
+}
+
+cudaError_t launch_quantize_mx4_rows(const uint16_t* x, const int32_t* perm, const int32_t* n_live, int64_t cap_rows,
+                                     int64_t cols, int k_div, uint8_t* Q, uint8_t* S, cudaStream_t st, int num_sms) {
+    const int64_t cap = (int64_t)num_sms * 8;
+    return launch_pdl(quantize_mx4_rows_kernel, dim3((unsigned)(cap_rows > cap ? cap : cap_rows)), dim3(kMxThreads), 0,
+                      st, x, perm, n_live, cap_rows, (int)cols, k_div, Q, S);
+}
+
+cudaError_t launch_dequantize_mx4(const uint8_t* Q, const uint8_t* S, int64_t elements, uint16_t* W, cudaStream_t st,
+                                  int num_sms) {
+    return launch_pdl(dequantize_mx4_kernel, dim3(mx_blocks(elements / 8, num_sms)), dim3(kMxThreads), 0, st, Q, S,
+                      elements / 8, W);
+}
+
+}  // namespace jmoe
