@@ -68,7 +68,7 @@ cudaError_t launch_quantize_mx4_rows(const uint16_t* x, const int32_t* perm, con
                                      int64_t cols, int k_div, uint8_t* Q, uint8_t* S, cudaStream_t st, int num_sms);
 cudaError_t launch_dequantize_mx4(const uint8_t* Q, const uint8_t* S, int64_t elements, uint16_t* W, cudaStream_t st,
                                   int num_sms);
-cudaError_t launch_grouped_mx4(const mx4::Args& p, cudaStream_t st);
+cudaError_t launch_grouped_mx4(const mx4::Args& p, cudaStream_t st, int num_sms);
 
 cudaError_t launch_tables_check(WsHeader* hdr, const int32_t* ids, const int32_t* perm, const int32_t* inv, int64_t TK,
                                 int64_t rows_cap, cudaStream_t st);
@@ -992,7 +992,7 @@ int jamba_moe_grouped_mx4(const uint8_t* xq, const uint8_t* xs, const int32_t* o
     p.M = (int)rows;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     TimedLaunch t(JMOE_KERNEL_GROUPED, st);
-    return to_status(launch_grouped_mx4(p, st));
+    return to_status(launch_grouped_mx4(p, st, num_sms_current()));
 }
 
 size_t jamba_moe_workspace_size_mx4(int64_t T, int64_t d, int64_t ffn, int n_experts, int top_k) {
@@ -1072,7 +1072,7 @@ int jamba_moe_forward_mx4(const uint16_t* x, const float* router_W, const float*
     p.M = (int)ffn;
     {
         TimedLaunch t(JMOE_KERNEL_GEMM13, st);
-        e = launch_grouped_mx4(p, st);
+        e = launch_grouped_mx4(p, st, sms);
     }
     if (e != cudaSuccess) return JMOE_ERR_CUDA;
     {
@@ -1094,7 +1094,7 @@ int jamba_moe_forward_mx4(const uint16_t* x, const float* router_W, const float*
     p.M = (int)d;
     {
         TimedLaunch t(JMOE_KERNEL_GEMM2, st);
-        e = launch_grouped_mx4(p, st);
+        e = launch_grouped_mx4(p, st, sms);
     }
     if (e != cudaSuccess) return JMOE_ERR_CUDA;
     {

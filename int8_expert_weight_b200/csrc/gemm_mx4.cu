@@ -1,0 +1,525 @@
+// Matrix products grouped by expert on MX4 operands (see quantize_mx4.cu for the format): the rows of
+// expert e, begin[e] .. begin[e] + count[e], are multiplied with that expert's weights,
+//
+//   plain   y[r][i]      = sum_k x^[r][k] W^_e[i][k]                   (bf16 or fp32)
+//   slot    out[a][i]    = p_a * sum_k x^[r][k] W^_e[i][k]             (fp32; a = assignment of row r)
+//   dual    h[r][j]      = bf16( SiLU(x^[r] . W1^_e[j]) * (x^[r] . W3^_e[j]) )
+//
+// with v^ the value of an MX4 code times its block's scale, fp32 sums.  The tensor cores take the codes
+// and the scales as they are (tcgen05.mma kind::mxf4.block_scale): nothing is expanded.
+//
+// One tile = 128 weight rows (the MMA's M, TMEM lanes) x up to kTok rows of one expert (N, TMEM
+// columns).  Weights as M: their 128-row tiles are always full, while the rows of an expert, often few,
+// only have to fill up a multiple of 16.  The rows of a group start anywhere: a copy of the tile reads past the
+// group's end into the next one's rows, whose columns of the result are not stored.
+//   dual: rows 32q .. 32q+15 of the tile are W1 rows j0+16q .., rows 32q+16 .. 32q+31 the W3 rows of the
+//   same j (q = 0..3), so gate and up of one j sit in lanes l and l + 16 of a warp and meet with one shuffle.
+//
+// Persistent, one CTA per SM, 384 threads in roles; a pipeline stage holds 256 of K (128 bytes of codes per row):
+//   warp 0      codes: TMA boxes of 128 bytes x 128 (dual: 16) weight rows and x 32 token rows, SWIZZLE_128B
+//   warps 2-3   scales: 4 bytes (128 of K) per row and copy, cp.async from the rows' own layout into the
+//               order that the tensor core wants (row r at 16 (r % 32) + 4 (r / 32) of a 512-byte block)
+//   warp 1      TMEM allocator; per stage copies the scales to TMEM (tcgen05.cp) and issues 4 MMAs of 64 k
+//   warps 4-11  epilogue: two warps per TMEM lane quarter, alternate 32-column chunks
+// TMEM: two accumulators of kTok columns, so a tile's epilogue overlaps the next tile's MMAs, and two
+// sets of scales.  Every mbarrier wait is bounded: on timeout the kernel records JMOE_DEV_TIMEOUT in the
+// workspace status word, the other roles stop at their next wait, in-flight copies and MMAs are waited for
+// (bounded), TMEM is released and the CTA returns.
+//
+// Tile order: expert by expert; inside an expert, bands of token tiles whose codes stay in L2 while every
+// weight tile streams past once per band; token tiles fastest, so the CTAs working at the same time share
+// each weight tile.  Tile i of a CTA is its index + i * grid.
+#include <cuda.h>
+
+#include "mx4.cuh"
+#include "tc.cuh"
+
+namespace jmoe {
+namespace mx4 {
+
+constexpr int kWRows = 128;
+constexpr int kStageBytes = 128;  // bytes of codes per row and stage: 256 of K
+constexpr int kBoxRows = 32;      // token rows per copy
+constexpr int kSfWarps = 2;
+constexpr int kEpiWarps = 8;
+constexpr int kEpiWarp0 = 2 + kSfWarps;
+constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
+constexpr uint32_t kMaxPolls = 1u << 22;  // ~0.3 s of polling: far above any healthy wait
+static_assert(kThreads >= kMaxGroups, "one thread per group");
+
+template <int kTok>
+struct Cfg {
+    static constexpr int kSfBlocks = (kTok + 127) / 128;  // 512-byte blocks of token scales per 128 k
+    static constexpr int kA = kWRows * kStageBytes;
+    static constexpr int kB = kTok * kStageBytes;
+    static constexpr int kSfA = 2 * 512;
+    static constexpr int kSfB = 2 * kSfBlocks * 512;
+    static constexpr int kStage = kA + kB + kSfA + kSfB;
+    static constexpr int kStages = (227 * 1024 - 8 * 1024) / kStage;
+    static constexpr int kSfCols = 8 + 8 * kSfBlocks;
+    static constexpr int kSfCol0 = 2 * kTok;
+    static constexpr uint32_t kTmemCols = kSfCol0 + 2 * kSfCols <= 256 ? 256 : 512;
+    static constexpr int kBars = 3 * kStages + 5;
+    static constexpr int kSmem = kStages * kStage + 1024 + 8 * kBars;
+    static_assert(kTok % 32 == 0 && kB % 1024 == 0 && kStages >= 3, "tile");
+    static_assert(kSfCol0 + 2 * kSfCols <= 512, "TMEM");
+};
+
+struct Tile {
+    int e, n;      // expert, weight tile
+    int64_t row0;  // first row of the token tile
+    int ntok;      // its rows (1 .. kTok)
+};
+
+// The group table of a call, in shared memory.
+struct Groups {
+    int tile0[kMaxGroups + 1];  // tiles of the groups before each
+    int count[kMaxGroups];
+    int row0[kMaxGroups];
+};
+
+template <int kTok>
+__device__ __forceinline__ void tile_at(const Groups& G, const Args& p, int L, Tile& t) {
+    int e = 0;  // the last group whose first tile is <= L: groups without rows have no tile
+#pragma unroll
+    for (int s = kMaxGroups / 2; s > 0; s >>= 1)
+        if (e + s < p.E && G.tile0[e + s] <= L) e += s;
+    const int count = G.count[e], local = L - G.tile0[e];
+    const int nt = (count + kTok - 1) / kTok;
+    const int tt = ((count + nt - 1) / nt + 15) & ~15;  // rows per token tile, as even as 16 allows
+    const int nb = (nt + p.band_max - 1) / p.band_max;
+    const int bfull = (nt + nb - 1) / nb;
+    const int band = local / (bfull * p.n_wt);
+    const int m_first = band * bfull;
+    const int bsz = min(bfull, nt - m_first);
+    const int within = local - band * bfull * p.n_wt;
+    const int m = m_first + within % bsz;
+    t.e = e;
+    t.n = within / bsz;
+    t.row0 = (int64_t)G.row0[e] + m * tt;
+    t.ntok = min(tt, count - m * tt);
+}
+
+// SiLU with the fast exponential and division intrinsics: a few fp32 ulps from the exact value,
+// far below the bf16 rounding of h that follows.
+__device__ __forceinline__ float silu_fast(float a) { return __fdividef(a, 1.0f + __expf(-a)); }
+
+__device__ __forceinline__ void fail(WsHeader* hdr, volatile int* abort) {
+    *abort = 1;
+    set_status(hdr, JMOE_DEV_TIMEOUT);
+}
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+template <bool kDual, int kTok>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_mx4_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW0,
+                    const __grid_constant__ CUtensorMap tmW1, Args p) {
+    using C = Cfg<kTok>;
+    constexpr int kStages = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Groups G;
+    __shared__ int warp_sum[kThreads / 32];
+    __shared__ uint32_t tmem_holder;
+    __shared__ volatile int abort_flag;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait();
+    // ---- group table: thread e takes group e
+    {
+        const int e = threadIdx.x;
+        int64_t row0 = 0;
+        int count = 0;
+        bool bad = false;
+        if (e < p.E) {
+            bad = group_at(p, e, row0, count);
+            G.count[e] = count;
+            G.row0[e] = (int)row0;
+        }
+        if (p.reset_status && blockIdx.x == 0) {
+            bad = __syncthreads_or(bad);
+            if (e == 0) p.hdr->status = bad ? JMOE_DEV_BAD_INDEX : JMOE_OK;
+        }
+        const int tiles = (count + kTok - 1) / kTok * p.n_wt;
+        int sum = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += v;
+        }
+        if (lane == 31) warp_sum[warp] = sum;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) sum += warp_sum[w];
+        if (e < p.E) G.tile0[e] = sum - tiles;
+        if (e == p.E - 1) G.tile0[p.E] = sum;
+        __syncthreads();
+    }
+    const int total = G.tile0[p.E];
+    if ((int)blockIdx.x >= total) return;  // no tile for this CTA: nothing was taken yet
+
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sA = smem;                          // [kStages][128 rows][128 B]
+    uint8_t* sB = sA + kStages * C::kA;          // [kStages][kTok rows][128 B]
+    uint8_t* sSA = sB + kStages * C::kB;         // [kStages][2][512 B]
+    uint8_t* sSB = sSA + kStages * C::kSfA;      // [kStages][2][kSfBlocks][512 B]
+    uint64_t* full_q = reinterpret_cast<uint64_t*>(sSB + kStages * C::kSfB);  // [kStages] codes landed
+    uint64_t* full_s = full_q + kStages;         // [kStages] scales landed
+    uint64_t* empty = full_s + kStages;          // [kStages] MMAs reading the stage are done
+    uint64_t* acc_full = empty + kStages;        // [2] accumulator complete
+    uint64_t* acc_empty = acc_full + 2;          // [2] accumulator read out by the epilogue
+    uint64_t* mma_done = acc_empty + 2;          // every issued MMA complete (teardown)
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            tc::mbar_init(&full_q[s], 1);
+            tc::mbar_init(&full_s[s], kSfWarps);
+            tc::mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            tc::mbar_init(&acc_full[b], 1);
+            tc::mbar_init(&acc_empty[b], kEpiWarps);
+        }
+        tc::mbar_init(mma_done, 1);
+        abort_flag = 0;
+        tc::mbar_fence_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tc::prefetch_tmap(&tmX);
+        tc::prefetch_tmap(&tmW0);
+        if (kDual) tc::prefetch_tmap(&tmW1);
+    }
+    if (warp == 1) tc::tmem_alloc(&tmem_holder, C::kTmemCols);
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = tmem_holder;
+    const int KW = p.K / 128;          // 4-byte words of scales per row
+    const int KB = (KW + 1) / 2;       // stages per tile; the last may hold one word only
+    int issued[kStages];               // codes: last round issued on each stage (-1: none)
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) issued[s] = -1;
+    int mma_issued = 0;
+    auto wait = [&](uint64_t* bar, int round) -> bool {
+        if (tc::mbar_wait_bounded(bar, round & 1, &abort_flag, kMaxPolls)) return true;
+        if (!abort_flag) fail(p.hdr, &abort_flag);
+        return false;
+    };
+
+    if (warp == 0) {
+        // ---------------- codes
+        if (lane == 0) {
+            int g = 0;
+            bool ok = true;
+            Tile t;
+            for (int L = blockIdx.x; ok && L < total; L += gridDim.x) {
+                tile_at<kTok>(G, p, L, t);
+                const int w_row0 = t.e * p.M + t.n * (kDual ? kWRows / 2 : kWRows);
+                const int n_box = (((t.ntok + 15) & ~15) + kBoxRows - 1) / kBoxRows;
+                for (int kb = 0; kb < KB; ++kb, ++g) {
+                    const int s = g % kStages, r = g / kStages;
+                    if (r > 0 && !(ok = wait(&empty[s], r - 1))) break;
+                    tc::mbar_arrive_expect_tx(&full_q[s], (uint32_t)(C::kA + n_box * kBoxRows * kStageBytes));
+                    uint8_t* da = sA + s * C::kA;
+                    uint8_t* db = sB + s * C::kB;
+                    const int x = kb * kStageBytes;
+                    if (kDual) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            tc::tma_load_2d(da + q * 32 * kStageBytes, &tmW0, &full_q[s], x, w_row0 + 16 * q);
+                            tc::tma_load_2d(da + (q * 32 + 16) * kStageBytes, &tmW1, &full_q[s], x, w_row0 + 16 * q);
+                        }
+                    } else {
+                        tc::tma_load_2d(da, &tmW0, &full_q[s], x, w_row0);
+                    }
+                    for (int i = 0; i < n_box; ++i)
+                        tc::tma_load_2d(db + i * kBoxRows * kStageBytes, &tmX, &full_q[s], x,
+                                        (int)t.row0 + i * kBoxRows);
+                    issued[s] = r;
+                }
+            }
+        }
+    } else if (warp < kEpiWarp0 && warp >= 2) {
+        // ---------------- scales: thread t of 64 takes rows t, t + 64, ...
+        constexpr int kRowsA = kWRows / 64, kRowsB = (kTok + 63) / 64;
+        const int tid = threadIdx.x - 64;
+        const int64_t stride = p.K / 32;
+        int g = 0;
+        bool ok = true;
+        Tile t;
+        for (int L = blockIdx.x; ok && L < total; L += gridDim.x) {
+            tile_at<kTok>(G, p, L, t);
+            const uint8_t *pa[kRowsA], *pb[kRowsB];
+            uint32_t da[kRowsA], db[kRowsB];
+#pragma unroll
+            for (int i = 0; i < kRowsA; ++i) {
+                const int r = tid + 64 * i;
+                // rows past the expert's last: any valid row, their results are not stored
+                const int j = kDual ? t.n * 64 + 16 * (r >> 5) + (r & 15) : t.n * kWRows + r;
+                const uint8_t* base = kDual && (r & 16) ? p.sb : p.sa;
+                pa[i] = base + ((int64_t)t.e * p.M + min(j, p.M - 1)) * stride;
+                da[i] = tc::smem_u32(sSA) + 16 * (r & 31) + 4 * (r >> 5);
+            }
+#pragma unroll
+            for (int i = 0; i < kRowsB; ++i) {
+                const int r = tid + 64 * i;
+                const int64_t row = t.row0 + r;
+                pb[i] = p.xs + (row < p.N ? row : p.N - 1) * stride;
+                db[i] = tc::smem_u32(sSB) + 512 * (r >> 7) + 16 * (r & 31) + 4 * ((r >> 5) & 3);
+            }
+            const int n_mma = (t.ntok + 15) & ~15;
+            for (int kb = 0; kb < KB; ++kb, ++g) {
+                const int s = g % kStages, r = g / kStages;
+                bool free_ = r == 0 || wait(&empty[s], r - 1);
+                if (!(ok = __all_sync(0xffffffffu, free_))) break;
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const int word = 2 * kb + w;
+                    if (word < KW) {
+#pragma unroll
+                        for (int i = 0; i < kRowsA; ++i)
+                            cp_async4(da[i] + s * C::kSfA + w * 512, pa[i] + 4 * word);
+#pragma unroll
+                        for (int i = 0; i < kRowsB; ++i)
+                            if (tid + 64 * i < n_mma)
+                                cp_async4(db[i] + s * C::kSfB + w * 512 * C::kSfBlocks, pb[i] + 4 * word);
+                    }
+                }
+                cp_async_commit();
+                // publish the stage before this one: its copies have had a stage's time to land
+                if (g > 0) {
+                    cp_async_wait<1>();
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&full_s[(g - 1) % kStages]);
+                }
+            }
+        }
+        cp_async_wait<0>();
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (ok && lane == 0) tc::mbar_arrive(&full_s[(g - 1) % kStages]);
+    } else if (warp == 1) {
+        // ---------------- MMA issuer
+        if (lane == 0) {
+            int g = 0, it = 0;
+            bool ok = true;
+            Tile t;
+            for (int L = blockIdx.x; L < total; L += gridDim.x, ++it) {
+                tile_at<kTok>(G, p, L, t);
+                const int n_mma = (t.ntok + 15) & ~15;
+                const uint32_t idesc0 = tc::idesc_mx4_f32(kWRows, n_mma, 0);
+                const uint32_t idesc2 = tc::idesc_mx4_f32(kWRows, n_mma, 2);
+                const int b = it & 1, u = it >> 1;
+                if (u > 0 && !(ok = wait(&acc_empty[b], u - 1))) break;
+                const uint32_t d_tmem = tmem + (uint32_t)(b * kTok);
+                for (int kb = 0; kb < KB; ++kb, ++g) {
+                    const int s = g % kStages, r = g / kStages;
+                    if (!(ok = wait(&full_q[s], r) && wait(&full_s[s], r))) break;
+                    // the scales' TMEM columns are those of stage g - 2: its MMAs have to be done
+                    if (g >= 2 && !(ok = wait(&empty[(g - 2) % kStages], (g - 2) / kStages))) break;
+                    tc::tc_fence_after();
+                    const uint32_t sf = tmem + C::kSfCol0 + (uint32_t)((g & 1) * C::kSfCols);
+                    const uint64_t adesc = tc::sw128_kmajor_desc(tc::smem_u32(sA + s * C::kA));
+                    const uint64_t bdesc = tc::sw128_kmajor_desc(tc::smem_u32(sB + s * C::kB));
+                    const uint64_t sadesc = tc::linear_desc(tc::smem_u32(sSA + s * C::kSfA));
+                    const uint64_t sbdesc = tc::linear_desc(tc::smem_u32(sSB + s * C::kSfB));
+                    const int words = min(2, KW - 2 * kb);
+                    for (int w = 0; w < words; ++w) {  // 512 bytes = +32 in a descriptor's address field
+                        const uint32_t sfa = sf + 4 * w, sfb = sf + 8 + 4 * C::kSfBlocks * w;
+                        tc::tmem_cp_32x16(sfa, sadesc + 32 * w);
+#pragma unroll
+                        for (int i = 0; i < C::kSfBlocks; ++i)
+                            tc::tmem_cp_32x16(sfb + 4 * i, sbdesc + 32 * (C::kSfBlocks * w + i));
+                        // 64 k = 32 bytes of the 128-byte row = +2 in the address field
+                        tc::mma_mx4_ss(d_tmem, adesc + 4 * w, bdesc + 4 * w, idesc0, sfa, sfb, (kb | w) != 0);
+                        tc::mma_mx4_ss(d_tmem, adesc + 4 * w + 2, bdesc + 4 * w + 2, idesc2, sfa, sfb, 1);
+                    }
+                    tc::mma_commit(&empty[s]);
+                    ++mma_issued;
+                }
+                if (!ok) break;
+                tc::mma_commit(&acc_full[b]);
+            }
+            tc::mma_commit(mma_done);  // arrives once every MMA issued above has completed
+        }
+        __syncwarp();
+    } else {
+        // ---------------- epilogue
+        const int qd = warp & 3, part = (warp - kEpiWarp0) >> 2;
+        int it = 0;
+        Tile t;
+        for (int L = blockIdx.x; L < total; L += gridDim.x, ++it) {
+            tile_at<kTok>(G, p, L, t);
+            const int b = it & 1, u = it >> 1;
+            const bool ok = wait(&acc_full[b], u);
+            if (!__all_sync(0xffffffffu, ok)) break;  // tcgen05.ld below is warp-collective
+            tc::tc_fence_after();
+            const uint32_t t_lane = tmem + ((uint32_t)(32 * qd) << 16) + (uint32_t)(b * kTok);
+            bool released = false;
+            auto release = [&]() {
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&acc_empty[b]);
+                released = true;
+            };
+#pragma unroll 1
+            for (int c = 32 * part; c < t.ntok; c += 64) {
+                uint32_t v[32];
+                tc::tmem_ld32(t_lane + (uint32_t)c, v);
+                tc::tmem_wait_ld();
+                if (c + 64 >= t.ntok) release();
+                if constexpr (kDual) {
+                    // lanes < 16 keep the gate of tokens c .. c+15 and take the up values from lane + 16;
+                    // lanes >= 16 keep the up of tokens c+16 .. c+31 and take the gate values from lane - 16
+                    const int j = t.n * 64 + 16 * qd + (lane & 15);
+                    const int tok0 = c + ((lane < 16) ? 0 : 16);
+                    uint16_t* hcol = p.y16 + (t.row0 + tok0) * p.M + j;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float own_keep = __uint_as_float(v[(lane < 16) ? i : 16 + i]);
+                        const float own_send = __uint_as_float(v[(lane < 16) ? 16 + i : i]);
+                        const float other = __shfl_xor_sync(0xffffffffu, own_send, 16);
+                        const float gt = (lane < 16) ? own_keep : other;
+                        const float up = (lane < 16) ? other : own_keep;
+                        if (tok0 + i < t.ntok && j < p.M)
+                            hcol[(int64_t)i * p.M] = f32_to_bf16_bits(silu_fast(gt) * up);
+                    }
+                } else {
+                    const int j = t.n * kWRows + 32 * qd + lane;
+                    if (p.wts) {
+                        const int32_t a_l = c + lane < t.ntok ? p.perm[t.row0 + c + lane] : -1;
+                        const float w_l = a_l >= 0 ? p.wts[a_l] : 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int32_t a = __shfl_sync(0xffffffffu, a_l, i);
+                            const float wt = __shfl_sync(0xffffffffu, w_l, i);
+                            if (a >= 0 && j < p.M) p.y32[(int64_t)a * p.M + j] = wt * __uint_as_float(v[i]);
+                        }
+                    } else if (p.y32) {
+                        float* ycol = p.y32 + (t.row0 + c) * p.M + j;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c + i < t.ntok && j < p.M) ycol[(int64_t)i * p.M] = __uint_as_float(v[i]);
+                    } else if (p.M & 1) {  // bf16 rows of odd length: no pair of them starts on 4 bytes throughout
+                        uint16_t* ycol = p.y16 + (t.row0 + c) * p.M + j;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c + i < t.ntok && j < p.M) ycol[(int64_t)i * p.M] = f32_to_bf16_bits(__uint_as_float(v[i]));
+                    } else {
+                        // neighbouring lanes trade: the even one stores columns j, j + 1 of even tokens, the odd one
+                        // columns j - 1, j of odd tokens, 4 bytes each
+                        const int odd = lane & 1;
+                        uint16_t* ycol = p.y16 + (t.row0 + c + odd) * p.M + (j - odd);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const float keep = __uint_as_float(odd ? v[i + 1] : v[i]);
+                            const float other = __shfl_xor_sync(0xffffffffu, __uint_as_float(odd ? v[i] : v[i + 1]), 1);
+                            const uint32_t lo = f32_to_bf16_bits(odd ? other : keep);
+                            const uint32_t hi = f32_to_bf16_bits(odd ? keep : other);
+                            if (c + i + odd < t.ntok && j < p.M)
+                                *reinterpret_cast<uint32_t*>(ycol + (int64_t)i * p.M) = lo | (hi << 16);
+                        }
+                    }
+                }
+            }
+            if (!released) release();  // a warp whose columns hold no tokens of this tile
+        }
+    }
+
+    // ---- teardown: after an abort, let in-flight copies and MMAs finish (bounded) before TMEM goes
+    pdl_trigger();
+    tc::tc_fence_before();
+    __syncthreads();
+    if (abort_flag) {
+        if (warp == 0 && lane == 0) {
+            for (int s = 0; s < kStages; ++s) {
+                if (issued[s] < 0) continue;
+                // a copy of round r completes phase r of full_q[s]; this wait ignores the abort flag
+                for (uint32_t i = 0; i < kMaxPolls && !tc::mbar_try_wait(&full_q[s], issued[s] & 1); ++i)
+                    __nanosleep(64);
+            }
+        }
+        if (warp == 1 && lane == 0 && mma_issued > 0) {
+            for (uint32_t i = 0; i < kMaxPolls && !tc::mbar_try_wait(mma_done, 0); ++i) __nanosleep(64);
+        }
+        __syncthreads();
+    }
+    if (warp == 1) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tmem, C::kTmemCols);
+    }
+}
+
+// ---------------------------------------------------------------- host side
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// Looked up once; the initialisation of a function-local static is thread-safe.
+EncodeTiledFn encode_fn() {
+    static const EncodeTiledFn fn = []() -> EncodeTiledFn {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<EncodeTiledFn>(f);
+        return nullptr;
+    }();
+    return fn;
+}
+
+// Codes [rows][K / 2], boxes of [box_rows][128 bytes]; what lies past the edges reads as zero.
+bool make_map(CUtensorMap* m, const uint8_t* ptr, uint64_t rows, uint64_t row_bytes, uint32_t box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {row_bytes, rows};
+    cuuint64_t strides[1] = {row_bytes};
+    cuuint32_t box[2] = {kStageBytes, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kDual, int kTok>
+cudaError_t launch(Args p, cudaStream_t st, int num_sms) {
+    using C = Cfg<kTok>;
+    CUtensorMap tx, tw0, tw1;
+    const uint64_t row_bytes = (uint64_t)p.K / 2, w_rows = (uint64_t)p.E * p.M;
+    constexpr uint32_t kWBox = kDual ? 16 : kWRows;
+    if (!make_map(&tx, p.xq, (uint64_t)p.N, row_bytes, kBoxRows) || !make_map(&tw0, p.qa, w_rows, row_bytes, kWBox) ||
+        !make_map(&tw1, kDual ? p.qb : p.qa, w_rows, row_bytes, kWBox))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(gemm_mx4_kernel<kDual, kTok>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         C::kSmem);
+    if (e != cudaSuccess) return e;
+    constexpr int kRows = kDual ? kWRows / 2 : kWRows;
+    p.n_wt = (p.M + kRows - 1) / kRows;
+    // token tiles per band: the band's codes near 32 MB of L2
+    const int64_t per_tile = (int64_t)kTok * (p.K / 2);
+    p.band_max = (int)(per_tile >= (32ll << 20) ? 1 : (32ll << 20) / per_tile);
+    // persistent: one CTA per SM, fewer when there cannot be that many tiles
+    int64_t grid = (p.N / kTok + (p.N < p.E ? p.N : p.E)) * p.n_wt;
+    if (grid > num_sms) grid = num_sms;
+    return launch_pdl(gemm_mx4_kernel<kDual, kTok>, dim3((unsigned)grid), dim3(kThreads), C::kSmem, st, tx, tw0, tw1,
+                      p);
+}
+
+}  // namespace mx4
+
+cudaError_t launch_grouped_mx4(const mx4::Args& p, cudaStream_t st, int num_sms) {
+    using namespace mx4;
+    // few rows per expert: narrow token tiles leave room for twice the stages, i.e. the weights in flight
+    const bool few = p.N <= (int64_t)48 * p.E;
+    if (p.qb) return few ? launch<true, 64>(p, st, num_sms) : launch<true, 224>(p, st, num_sms);
+    return few ? launch<false, 64>(p, st, num_sms) : launch<false, 224>(p, st, num_sms);
+}
+
+}  // namespace jmoe

@@ -27,21 +27,18 @@ struct Args {
     float* y32;            // plain: y in fp32; slot: out [T*K][M]
     int K;                 // reduction length
     int M;                 // weight rows per expert and matrix
+    int n_wt;              // weight tiles per expert (set by the launcher)
+    int band_max;          // token tiles per L2 band, at most (set by the launcher)
 };
 
 // Rows of expert e.  Whatever the table holds, [row0, row0 + count) lies inside the N rows of x and y.
-__device__ __forceinline__ void group_at(const Args& p, int e, int64_t& row0, int& count) {
+// Returns whether its entries break the rule 0 <= begin, count >= 0, begin + count <= N.
+__device__ __forceinline__ bool group_at(const Args& p, int e, int64_t& row0, int& count) {
     const int64_t b = p.begin[e];
     const int64_t c = p.count ? p.count[e] : p.begin[e + 1] - b;
     row0 = b < 0 ? 0 : (b > p.N ? p.N : b);
     count = (int)(c < 0 ? 0 : (c > p.N - row0 ? p.N - row0 : c));
-}
-
-// Status of a caller's offsets: 0 <= begin[0] <= ... <= begin[E] <= N, or JMOE_DEV_BAD_INDEX.  By one thread.
-__device__ __forceinline__ void check_groups(const Args& p) {
-    bool bad = p.begin[0] < 0 || p.begin[p.E] > p.N;
-    for (int e = 0; e < p.E; ++e) bad |= p.begin[e] > p.begin[e + 1];
-    p.hdr->status = bad ? JMOE_DEV_BAD_INDEX : JMOE_OK;
+    return b != row0 || c != count;
 }
 
 }  // namespace mx4

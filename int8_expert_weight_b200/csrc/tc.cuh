@@ -128,6 +128,22 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// D[tmem] (+)= A[smem desc] * B[smem desc]^T with E2M1 operands and one E8M0 scale per row and 32 k
+// (kind::mxf4, K = 64 per instruction); sfa, sfb: TMEM addresses of the scales (see idesc_mx4_f32).
+__device__ __forceinline__ void mma_mx4_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+// 32 rows of 16 bytes from shared memory (512 contiguous bytes: linear_desc) to 4 TMEM columns, the
+// same in each of the four 32-lane quarters.  Ordered before later MMAs of the same thread.
+__device__ __forceinline__ void tmem_cp_32x16(uint32_t taddr, uint64_t sdesc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
 // Arrive once on the mbarrier when all previously issued MMAs of this thread have completed.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
@@ -177,6 +193,30 @@ __device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t smem_addr) {
     d |= (uint64_t)1 << 46;                        // version
     d |= (uint64_t)2 << 61;                        // SWIZZLE_128B
     return d;
+}
+
+// Shared-memory descriptor of rows of 16 bytes back to back, no swizzle: 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t linear_desc(uint32_t smem_addr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((smem_addr & 0x3FFFF) >> 4);  // start address
+    d |= (uint64_t)1 << 16;                        // leading byte offset (one 16-byte column: unused)
+    d |= (uint64_t)(128 >> 4) << 32;               // stride byte offset
+    d |= (uint64_t)1 << 46;                        // version
+    return d;
+}
+
+// Instruction descriptor for kind::mxf4: E2M1 A and B, both K-major, E8M0 scales, fp32 D, shape M x N
+// (M = 128).  A 32-bit TMEM cell holds four consecutive scales of one row (k blocks of 32); row r is in
+// lane r % 32 (of every quarter), column r / 32.  An instruction (two blocks) takes the scales in bytes
+// `pair` and pair + 1 of the cells, pair = 0 or 2.
+__host__ __device__ constexpr uint32_t idesc_mx4_f32(int M, int N, int pair) {
+    return ((uint32_t)pair << 4)            // B scale byte
+           | (1u << 7)                      // A format: E2M1
+           | (1u << 10)                     // B format: E2M1
+           | ((uint32_t)(N >> 3) << 17)     // N / 8
+           | (1u << 23)                     // scale format: E8M0
+           | ((uint32_t)(M >> 7) << 27)     // M / 128
+           | ((uint32_t)pair << 29);        // A scale byte
 }
 
 // Instruction descriptor for kind::f8f6f4 with both operands E4M3 (format code 0), fp32
