@@ -15,14 +15,17 @@
 //   dual: rows 32q .. 32q+15 of the tile are W1 rows j0+16q .., rows 32q+16 .. 32q+31 the W3 rows of the
 //   same j (q = 0..3), so gate and up of one j sit in lanes l and l + 16 of a warp and meet with one shuffle.
 //
-// Persistent, one CTA per SM, 384 threads in roles; a pipeline stage holds 256 of K (128 bytes of codes per row):
+// Persistent, one CTA per SM, warps in roles; a pipeline stage holds 256 of K (128 bytes of codes per row):
 //   warp 0      codes: TMA boxes of 128 bytes x 128 (dual: 16) weight rows and x 32 token rows, SWIZZLE_128B
-//   warps 2-3   scales: 4 bytes (128 of K) per row and copy, cp.async from the rows' own layout into the
-//               order that the tensor core wants (row r at 16 (r % 32) + 4 (r / 32) of a 512-byte block)
 //   warp 1      TMEM allocator; per stage copies the scales to TMEM (tcgen05.cp) and issues 4 MMAs of 64 k
-//   warps 4-11  epilogue: two warps per TMEM lane quarter, alternate 32-column chunks
-// TMEM: two accumulators of kTok columns, so a tile's epilogue overlaps the next tile's MMAs, and two
-// sets of scales.  Every mbarrier wait is bounded: on timeout the kernel records JMOE_DEV_TIMEOUT in the
+//   2-3 warps   scales: one warp per 128 rows of weights or tokens.  The tensor core wants 512-byte blocks of 128 rows
+//               x 128 k with row r at 16 (r % 32) + 4 (r / 32); a lane reads 32 bytes (a DRAM sector: 1024 of
+//               K, four stages) of rows lane, lane + 32, + 64, + 96 into registers, four stages ahead and across
+//               tiles, and stores 16 bytes per block.  (4-byte copies per row and 128 k fetched each sector
+//               eight times: 2.85 TB/s instead of 5.0 on the 64-token product.)
+//   8 warps     epilogue: two warps per TMEM lane quarter, alternate 32-column chunks
+// TMEM: two accumulators of kTok columns, so a tile's epilogue overlaps the next tile's MMAs, and a set
+// of scales per stage.  Every mbarrier wait is bounded: on timeout the kernel records JMOE_DEV_TIMEOUT in the
 // workspace status word, the other roles stop at their next wait, in-flight copies and MMAs are waited for
 // (bounded), TMEM is released and the CTA returns.
 //
@@ -40,12 +43,9 @@ namespace mx4 {
 constexpr int kWRows = 128;
 constexpr int kStageBytes = 128;  // bytes of codes per row and stage: 256 of K
 constexpr int kBoxRows = 32;      // token rows per copy
-constexpr int kSfWarps = 2;
 constexpr int kEpiWarps = 8;
-constexpr int kEpiWarp0 = 2 + kSfWarps;
-constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
+constexpr int kSfStages = 4;      // stages whose scales a lane holds: 32 bytes of each of its rows
 constexpr uint32_t kMaxPolls = 1u << 22;  // ~0.3 s of polling: far above any healthy wait
-static_assert(kThreads >= kMaxGroups, "one thread per group");
 
 template <int kTok>
 struct Cfg {
@@ -58,11 +58,15 @@ struct Cfg {
     static constexpr int kStages = (227 * 1024 - 8 * 1024) / kStage;
     static constexpr int kSfCols = 8 + 8 * kSfBlocks;
     static constexpr int kSfCol0 = 2 * kTok;
-    static constexpr uint32_t kTmemCols = kSfCol0 + 2 * kSfCols <= 256 ? 256 : 512;
-    static constexpr int kBars = 3 * kStages + 5;
+    static constexpr uint32_t kTmemCols = kSfCol0 + kStages * kSfCols <= 256 ? 256 : 512;
+    static constexpr int kSfWarps = 1 + kSfBlocks;
+    static constexpr int kEpiWarp0 = 2 + kSfWarps;
+    static constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
+    static constexpr int kBars = 2 * kStages + 5;
     static constexpr int kSmem = kStages * kStage + 1024 + 8 * kBars;
-    static_assert(kTok % 32 == 0 && kB % 1024 == 0 && kStages >= 3, "tile");
-    static_assert(kSfCol0 + 2 * kSfCols <= 512, "TMEM");
+    static_assert(kThreads >= kMaxGroups, "one thread per group");
+    static_assert(kTok % 16 == 0 && kB % 1024 == 0 && kStages >= 3, "tile");
+    static_assert(kSfCol0 + kStages * kSfCols <= 512, "TMEM");
 };
 
 struct Tile {
@@ -86,7 +90,6 @@ __device__ __forceinline__ void tile_at(const Groups& G, const Args& p, int L, T
         if (e + s < p.E && G.tile0[e + s] <= L) e += s;
     const int count = G.count[e], local = L - G.tile0[e];
     const int nt = (count + kTok - 1) / kTok;
-    const int tt = ((count + nt - 1) / nt + 15) & ~15;  // rows per token tile, as even as 16 allows
     const int nb = (nt + p.band_max - 1) / p.band_max;
     const int bfull = (nt + nb - 1) / nb;
     const int band = local / (bfull * p.n_wt);
@@ -96,8 +99,8 @@ __device__ __forceinline__ void tile_at(const Groups& G, const Args& p, int L, T
     const int m = m_first + within % bsz;
     t.e = e;
     t.n = within / bsz;
-    t.row0 = (int64_t)G.row0[e] + m * tt;
-    t.ntok = min(tt, count - m * tt);
+    t.row0 = (int64_t)G.row0[e] + m * kTok;
+    t.ntok = min(kTok, count - m * kTok);
 }
 
 // SiLU with the fast exponential and division intrinsics: a few fp32 ulps from the exact value,
@@ -109,28 +112,32 @@ __device__ __forceinline__ void fail(WsHeader* hdr, volatile int* abort) {
     set_status(hdr, JMOE_DEV_TIMEOUT);
 }
 
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kPending>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+// 32 bytes of scales; `vec`: 32-byte aligned and whole, else `words` 4-byte words of them are there.
+__device__ __forceinline__ void ld_scales(const uint8_t* ptr, bool vec, int words, uint32_t (&v)[2 * kSfStages]) {
+    if (vec) {
+        asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                     : "l"(ptr));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2 * kSfStages; ++i)
+            v[i] = i < words ? __ldg(reinterpret_cast<const uint32_t*>(ptr) + i) : 0u;
+    }
 }
 
 template <bool kDual, int kTok>
-__global__ void __launch_bounds__(kThreads, 1)
-    gemm_mx4_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW0,
-                    const __grid_constant__ CUtensorMap tmW1, Args p) {
+__global__ void __launch_bounds__(Cfg<kTok>::kThreads, 1)
+    gemm_mx4_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXs,
+                    const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUtensorMap tmW1, Args p) {
     using C = Cfg<kTok>;
-    constexpr int kStages = C::kStages;
+    constexpr int kStages = C::kStages, kEpiWarp0 = C::kEpiWarp0;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Groups G;
-    __shared__ int warp_sum[kThreads / 32];
+    __shared__ int warp_sum[C::kThreads / 32];
     __shared__ uint32_t tmem_holder;
     __shared__ volatile int abort_flag;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
     pdl_wait();
     // ---- group table: thread e takes group e
     {
@@ -169,17 +176,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* sB = sA + kStages * C::kA;          // [kStages][kTok rows][128 B]
     uint8_t* sSA = sB + kStages * C::kB;         // [kStages][2][512 B]
     uint8_t* sSB = sSA + kStages * C::kSfA;      // [kStages][2][kSfBlocks][512 B]
-    uint64_t* full_q = reinterpret_cast<uint64_t*>(sSB + kStages * C::kSfB);  // [kStages] codes landed
-    uint64_t* full_s = full_q + kStages;         // [kStages] scales landed
-    uint64_t* empty = full_s + kStages;          // [kStages] MMAs reading the stage are done
+    uint64_t* full = reinterpret_cast<uint64_t*>(sSB + kStages * C::kSfB);  // [kStages] codes and scales are there
+    uint64_t* empty = full + kStages;            // [kStages] MMAs reading the stage are done
     uint64_t* acc_full = empty + kStages;        // [2] accumulator complete
     uint64_t* acc_empty = acc_full + 2;          // [2] accumulator read out by the epilogue
     uint64_t* mma_done = acc_empty + 2;          // every issued MMA complete (teardown)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            tc::mbar_init(&full_q[s], 1);
-            tc::mbar_init(&full_s[s], kSfWarps);
+            tc::mbar_init(&full[s], 1 + C::kSfWarps);
             tc::mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -192,6 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == 0 && lane == 0) {
         tc::prefetch_tmap(&tmX);
+        tc::prefetch_tmap(&tmXs);
         tc::prefetch_tmap(&tmW0);
         if (kDual) tc::prefetch_tmap(&tmW1);
     }
@@ -202,10 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = tmem_holder;
     const int KW = p.K / 128;          // 4-byte words of scales per row
     const int KB = (KW + 1) / 2;       // stages per tile; the last may hold one word only
-    int issued[kStages];               // codes: last round issued on each stage (-1: none)
-#pragma unroll
-    for (int s = 0; s < kStages; ++s) issued[s] = -1;
-    int mma_issued = 0;
+    int issued = 0;                    // codes: stages copied; MMA issuer: stages multiplied
     auto wait = [&](uint64_t* bar, int round) -> bool {
         if (tc::mbar_wait_bounded(bar, round & 1, &abort_flag, kMaxPolls)) return true;
         if (!abort_flag) fail(p.hdr, &abort_flag);
@@ -214,141 +217,161 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0) {
         // ---------------- codes
-        if (lane == 0) {
-            int g = 0;
-            bool ok = true;
-            Tile t;
-            for (int L = blockIdx.x; ok && L < total; L += gridDim.x) {
-                tile_at<kTok>(G, p, L, t);
-                const int w_row0 = t.e * p.M + t.n * (kDual ? kWRows / 2 : kWRows);
-                const int n_box = (((t.ntok + 15) & ~15) + kBoxRows - 1) / kBoxRows;
-                for (int kb = 0; kb < KB; ++kb, ++g) {
-                    const int s = g % kStages, r = g / kStages;
-                    if (r > 0 && !(ok = wait(&empty[s], r - 1))) break;
-                    tc::mbar_arrive_expect_tx(&full_q[s], (uint32_t)(C::kA + n_box * kBoxRows * kStageBytes));
-                    uint8_t* da = sA + s * C::kA;
-                    uint8_t* db = sB + s * C::kB;
-                    const int x = kb * kStageBytes;
-                    if (kDual) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            tc::tma_load_2d(da + q * 32 * kStageBytes, &tmW0, &full_q[s], x, w_row0 + 16 * q);
-                            tc::tma_load_2d(da + (q * 32 + 16) * kStageBytes, &tmW1, &full_q[s], x, w_row0 + 16 * q);
-                        }
-                    } else {
-                        tc::tma_load_2d(da, &tmW0, &full_q[s], x, w_row0);
-                    }
-                    for (int i = 0; i < n_box; ++i)
-                        tc::tma_load_2d(db + i * kBoxRows * kStageBytes, &tmX, &full_q[s], x,
-                                        (int)t.row0 + i * kBoxRows);
-                    issued[s] = r;
-                }
-            }
-        }
-    } else if (warp < kEpiWarp0 && warp >= 2) {
-        // ---------------- scales: thread t of 64 takes rows t, t + 64, ...
-        constexpr int kRowsA = kWRows / 64, kRowsB = (kTok + 63) / 64;
-        const int tid = threadIdx.x - 64;
-        const int64_t stride = p.K / 32;
         int g = 0;
         bool ok = true;
         Tile t;
         for (int L = blockIdx.x; ok && L < total; L += gridDim.x) {
             tile_at<kTok>(G, p, L, t);
-            const uint8_t *pa[kRowsA], *pb[kRowsB];
-            uint32_t da[kRowsA], db[kRowsB];
-#pragma unroll
-            for (int i = 0; i < kRowsA; ++i) {
-                const int r = tid + 64 * i;
-                // rows past the expert's last: any valid row, their results are not stored
-                const int j = kDual ? t.n * 64 + 16 * (r >> 5) + (r & 15) : t.n * kWRows + r;
-                const uint8_t* base = kDual && (r & 16) ? p.sb : p.sa;
-                pa[i] = base + ((int64_t)t.e * p.M + min(j, p.M - 1)) * stride;
-                da[i] = tc::smem_u32(sSA) + 16 * (r & 31) + 4 * (r >> 5);
-            }
-#pragma unroll
-            for (int i = 0; i < kRowsB; ++i) {
-                const int r = tid + 64 * i;
-                const int64_t row = t.row0 + r;
-                pb[i] = p.xs + (row < p.N ? row : p.N - 1) * stride;
-                db[i] = tc::smem_u32(sSB) + 512 * (r >> 7) + 16 * (r & 31) + 4 * ((r >> 5) & 3);
-            }
-            const int n_mma = (t.ntok + 15) & ~15;
+            const int w_row0 = t.e * p.M + t.n * (kDual ? kWRows / 2 : kWRows);
+            // one copy for a tile (nearly) full of tokens, else the 32-row boxes it needs
+            const int n_box = t.ntok > kTok / kBoxRows * kBoxRows - kBoxRows ? 0 : (t.ntok + kBoxRows - 1) / kBoxRows;
+            const uint32_t bytes = C::kA + (n_box == 0 ? kTok : n_box * kBoxRows) * kStageBytes;
             for (int kb = 0; kb < KB; ++kb, ++g) {
                 const int s = g % kStages, r = g / kStages;
-                bool free_ = r == 0 || wait(&empty[s], r - 1);
+                if (r > 0 && !(ok = wait(&empty[s], r - 1))) break;
+                uint8_t* da = sA + s * C::kA;
+                uint8_t* db = sB + s * C::kB;
+                const int x = kb * kStageBytes;
+                if (tc::elect_one()) {
+                    tc::mbar_arrive_expect_tx(&full[s], bytes);
+                    if (kDual) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            tc::tma_load_2d(da + q * 32 * kStageBytes, &tmW0, &full[s], x, w_row0 + 16 * q);
+                            tc::tma_load_2d(da + (q * 32 + 16) * kStageBytes, &tmW1, &full[s], x, w_row0 + 16 * q);
+                        }
+                    } else {
+                        tc::tma_load_2d(da, &tmW0, &full[s], x, w_row0);
+                    }
+                    if (n_box == 0) tc::tma_load_2d(db, &tmX, &full[s], x, (int)t.row0);
+                    for (int i = 0; i < n_box; ++i)
+                        tc::tma_load_2d(db + i * kBoxRows * kStageBytes, &tmXs, &full[s], x,
+                                        (int)t.row0 + i * kBoxRows);
+                }
+                __syncwarp();
+                issued = g + 1;
+            }
+        }
+    } else if (warp < kEpiWarp0 && warp >= 2) {
+        // ---------------- scales: warp 2 those of the weights, each other warp 128 token rows
+        const int blk = warp - 3;
+        const int64_t stride = p.K / 32;
+        const uint32_t dst0 = tc::smem_u32(blk < 0 ? sSA : sSB + 512 * blk) + 16 * lane;
+        const uint32_t dst_stage = blk < 0 ? C::kSfA : C::kSfB;
+        const uint32_t dst_word = blk < 0 ? 512 : 512 * C::kSfBlocks;
+        // what is loaded next: rows 32 i + lane (i < live) of tile L, from stage kb on
+        const uint8_t* ptr[4] = {};
+        int L = blockIdx.x, kb = 0, live = 0;
+        auto open_tile = [&]() {
+            Tile t;
+            tile_at<kTok>(G, p, L, t);
+            const int n_mma = (t.ntok + 15) & ~15;
+            live = blk < 0 ? 4 : max(0, min(4, (n_mma - 128 * blk + 31) / 32));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 32 * i + lane;
+                // rows past the expert's (or the matrix's) last: any valid row, their results are not stored
+                if (blk < 0) {
+                    const int j = kDual ? t.n * 64 + 16 * i + (lane & 15) : t.n * kWRows + r;
+                    ptr[i] = (kDual && lane >= 16 ? p.sb : p.sa) + ((int64_t)t.e * p.M + min(j, p.M - 1)) * stride;
+                } else {
+                    const int64_t row = t.row0 + 128 * blk + r;
+                    ptr[i] = p.xs + (row < p.N ? row : p.N - 1) * stride;
+                }
+            }
+        };
+        auto fetch = [&](uint32_t (&v)[4][2 * kSfStages]) -> int {  // returns the stages held (0: past the last tile)
+            if (L >= total) return 0;
+            if (kb == 0) open_tile();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < live) ld_scales(ptr[i] + 8 * kb, p.vec_scales, KW - 2 * kb, v[i]);
+            const int n = min(kSfStages, KB - kb);
+            kb += kSfStages;
+            if (kb >= KB) {
+                kb = 0;
+                L += gridDim.x;
+            }
+            return n;
+        };
+        uint32_t cur[4][2 * kSfStages] = {}, nxt[4][2 * kSfStages] = {};
+        int g = 0;
+        bool ok = true;
+        for (int n = fetch(cur); ok && n > 0;) {
+            const int n_next = fetch(nxt);
+#pragma unroll
+            for (int st = 0; st < kSfStages; ++st) {
+                if (st >= n) break;
+                const int s = g % kStages, r = g / kStages;
+                const bool free_ = r == 0 || wait(&empty[s], r - 1);
                 if (!(ok = __all_sync(0xffffffffu, free_))) break;
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const int word = 2 * kb + w;
-                    if (word < KW) {
-#pragma unroll
-                        for (int i = 0; i < kRowsA; ++i)
-                            cp_async4(da[i] + s * C::kSfA + w * 512, pa[i] + 4 * word);
-#pragma unroll
-                        for (int i = 0; i < kRowsB; ++i)
-                            if (tid + 64 * i < n_mma)
-                                cp_async4(db[i] + s * C::kSfB + w * 512 * C::kSfBlocks, pb[i] + 4 * word);
-                    }
-                }
-                cp_async_commit();
-                // publish the stage before this one: its copies have had a stage's time to land
-                if (g > 0) {
-                    cp_async_wait<1>();
-                    tc::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&full_s[(g - 1) % kStages]);
-                }
+                for (int w = 0; w < 2; ++w)
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst0 + s * dst_stage + w * dst_word),
+                                 "r"(cur[0][2 * st + w]), "r"(cur[1][2 * st + w]), "r"(cur[2][2 * st + w]),
+                                 "r"(cur[3][2 * st + w])
+                                 : "memory");
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&full[s]);
+                ++g;
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 2 * kSfStages; ++j) cur[i][j] = nxt[i][j];
+            n = n_next;
         }
-        cp_async_wait<0>();
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (ok && lane == 0) tc::mbar_arrive(&full_s[(g - 1) % kStages]);
     } else if (warp == 1) {
-        // ---------------- MMA issuer
-        if (lane == 0) {
-            int g = 0, it = 0;
-            bool ok = true;
-            Tile t;
-            for (int L = blockIdx.x; L < total; L += gridDim.x, ++it) {
-                tile_at<kTok>(G, p, L, t);
-                const int n_mma = (t.ntok + 15) & ~15;
-                const uint32_t idesc0 = tc::idesc_mx4_f32(kWRows, n_mma, 0);
-                const uint32_t idesc2 = tc::idesc_mx4_f32(kWRows, n_mma, 2);
-                const int b = it & 1, u = it >> 1;
-                if (u > 0 && !(ok = wait(&acc_empty[b], u - 1))) break;
-                const uint32_t d_tmem = tmem + (uint32_t)(b * kTok);
-                for (int kb = 0; kb < KB; ++kb, ++g) {
-                    const int s = g % kStages, r = g / kStages;
-                    if (!(ok = wait(&full_q[s], r) && wait(&full_s[s], r))) break;
-                    // the scales' TMEM columns are those of stage g - 2: its MMAs have to be done
-                    if (g >= 2 && !(ok = wait(&empty[(g - 2) % kStages], (g - 2) / kStages))) break;
-                    tc::tc_fence_after();
-                    const uint32_t sf = tmem + C::kSfCol0 + (uint32_t)((g & 1) * C::kSfCols);
-                    const uint64_t adesc = tc::sw128_kmajor_desc(tc::smem_u32(sA + s * C::kA));
-                    const uint64_t bdesc = tc::sw128_kmajor_desc(tc::smem_u32(sB + s * C::kB));
-                    const uint64_t sadesc = tc::linear_desc(tc::smem_u32(sSA + s * C::kSfA));
-                    const uint64_t sbdesc = tc::linear_desc(tc::smem_u32(sSB + s * C::kSfB));
-                    const int words = min(2, KW - 2 * kb);
-                    for (int w = 0; w < words; ++w) {  // 512 bytes = +32 in a descriptor's address field
-                        const uint32_t sfa = sf + 4 * w, sfb = sf + 8 + 4 * C::kSfBlocks * w;
-                        tc::tmem_cp_32x16(sfa, sadesc + 32 * w);
+        // ---------------- MMA issuer: the warp stays converged, one elected lane issues
+        const uint64_t adesc0 = tc::sw128_kmajor_desc(tc::smem_u32(sA)), bdesc0 = tc::sw128_kmajor_desc(tc::smem_u32(sB));
+        const uint64_t sadesc0 = tc::linear_desc(tc::smem_u32(sSA)), sbdesc0 = tc::linear_desc(tc::smem_u32(sSB));
+        int g = 0, it = 0;
+        bool ok = true;
+        Tile t;
+        for (int L = blockIdx.x; L < total; L += gridDim.x, ++it) {
+            tile_at<kTok>(G, p, L, t);
+            const int n_mma = (t.ntok + 15) & ~15;
+            const uint32_t idesc0 = tc::idesc_mx4_f32(kWRows, n_mma, 0);
+            const uint32_t idesc2 = tc::idesc_mx4_f32(kWRows, n_mma, 2);
+            const int b = it & 1, u = it >> 1;
+            if (u > 0 && !(ok = wait(&acc_empty[b], u - 1))) break;
+            const uint32_t d_tmem = tmem + (uint32_t)(b * kTok);
+            for (int kb = 0; kb < KB; ++kb, ++g) {
+                const int s = g % kStages, r = g / kStages;
+                if (!(ok = wait(&full[s], r))) break;
+                tc::tc_fence_after();
+                if (tc::elect_one()) {
+                    const uint32_t sf = tmem + C::kSfCol0 + (uint32_t)(s * C::kSfCols);
+                    const uint64_t adesc = adesc0 + (uint32_t)(s * (C::kA >> 4)), bdesc = bdesc0 + (uint32_t)(s * (C::kB >> 4));
+                    const uint64_t sadesc = sadesc0 + (uint32_t)(s * (C::kSfA >> 4));
+                    const uint64_t sbdesc = sbdesc0 + (uint32_t)(s * (C::kSfB >> 4));
+                    // 512 bytes = +32 in a descriptor's address field; the second 128 k of a last stage need not be there
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        tc::tmem_cp_32x16(sf + 4 * w, sadesc + 32 * w);
 #pragma unroll
                         for (int i = 0; i < C::kSfBlocks; ++i)
-                            tc::tmem_cp_32x16(sfb + 4 * i, sbdesc + 32 * (C::kSfBlocks * w + i));
-                        // 64 k = 32 bytes of the 128-byte row = +2 in the address field
-                        tc::mma_mx4_ss(d_tmem, adesc + 4 * w, bdesc + 4 * w, idesc0, sfa, sfb, (kb | w) != 0);
-                        tc::mma_mx4_ss(d_tmem, adesc + 4 * w + 2, bdesc + 4 * w + 2, idesc2, sfa, sfb, 1);
+                            tc::tmem_cp_32x16(sf + 8 + 4 * (C::kSfBlocks * w + i), sbdesc + 32 * (C::kSfBlocks * w + i));
+                    }
+                    // 64 k = 32 bytes of the 128-byte row = +2 in the address field
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        if (w == 0 || 2 * kb + 1 < KW) {
+                            const uint32_t sfa = sf + 4 * w, sfb = sf + 8 + 4 * C::kSfBlocks * w;
+                            tc::mma_mx4_ss(d_tmem, adesc + 4 * w, bdesc + 4 * w, idesc0, sfa, sfb, (kb | w) != 0);
+                            tc::mma_mx4_ss(d_tmem, adesc + 4 * w + 2, bdesc + 4 * w + 2, idesc2, sfa, sfb, 1);
+                        }
                     }
                     tc::mma_commit(&empty[s]);
-                    ++mma_issued;
+                    if (kb == KB - 1) tc::mma_commit(&acc_full[b]);
                 }
-                if (!ok) break;
-                tc::mma_commit(&acc_full[b]);
+                __syncwarp();
+                issued = g + 1;
             }
-            tc::mma_commit(mma_done);  // arrives once every MMA issued above has completed
+            if (!ok) break;
         }
+        if (tc::elect_one()) tc::mma_commit(mma_done);  // arrives once every MMA issued above has completed
         __syncwarp();
     } else {
         // ---------------- epilogue
@@ -440,13 +463,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (abort_flag) {
         if (warp == 0 && lane == 0) {
             for (int s = 0; s < kStages; ++s) {
-                if (issued[s] < 0) continue;
-                // a copy of round r completes phase r of full_q[s]; this wait ignores the abort flag
-                for (uint32_t i = 0; i < kMaxPolls && !tc::mbar_try_wait(&full_q[s], issued[s] & 1); ++i)
+                if (s >= issued) continue;
+                const int last = (issued - 1 - s) / kStages;
+                // a copy of round r completes phase `last` of full[s] once the scales are there too, else this wait runs out
+                for (uint32_t i = 0; i < kMaxPolls && !tc::mbar_try_wait(&full[s], last & 1); ++i)
                     __nanosleep(64);
             }
         }
-        if (warp == 1 && lane == 0 && mma_issued > 0) {
+        if (warp == 1 && lane == 0 && issued > 0) {
             for (uint32_t i = 0; i < kMaxPolls && !tc::mbar_try_wait(mma_done, 0); ++i) __nanosleep(64);
         }
         __syncthreads();
@@ -491,10 +515,11 @@ bool make_map(CUtensorMap* m, const uint8_t* ptr, uint64_t rows, uint64_t row_by
 template <bool kDual, int kTok>
 cudaError_t launch(Args p, cudaStream_t st, int num_sms) {
     using C = Cfg<kTok>;
-    CUtensorMap tx, tw0, tw1;
+    CUtensorMap tx, txs, tw0, tw1;
     const uint64_t row_bytes = (uint64_t)p.K / 2, w_rows = (uint64_t)p.E * p.M;
     constexpr uint32_t kWBox = kDual ? 16 : kWRows;
-    if (!make_map(&tx, p.xq, (uint64_t)p.N, row_bytes, kBoxRows) || !make_map(&tw0, p.qa, w_rows, row_bytes, kWBox) ||
+    if (!make_map(&tx, p.xq, (uint64_t)p.N, row_bytes, kTok) ||
+        !make_map(&txs, p.xq, (uint64_t)p.N, row_bytes, kBoxRows) || !make_map(&tw0, p.qa, w_rows, row_bytes, kWBox) ||
         !make_map(&tw1, kDual ? p.qb : p.qa, w_rows, row_bytes, kWBox))
         return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(gemm_mx4_kernel<kDual, kTok>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -502,14 +527,17 @@ cudaError_t launch(Args p, cudaStream_t st, int num_sms) {
     if (e != cudaSuccess) return e;
     constexpr int kRows = kDual ? kWRows / 2 : kWRows;
     p.n_wt = (p.M + kRows - 1) / kRows;
+    const uintptr_t scales = reinterpret_cast<uintptr_t>(p.xs) | reinterpret_cast<uintptr_t>(p.sa) |
+                             reinterpret_cast<uintptr_t>(kDual ? p.sb : p.sa);
+    p.vec_scales = p.K % 1024 == 0 && scales % 32 == 0;
     // token tiles per band: the band's codes near 32 MB of L2
     const int64_t per_tile = (int64_t)kTok * (p.K / 2);
     p.band_max = (int)(per_tile >= (32ll << 20) ? 1 : (32ll << 20) / per_tile);
     // persistent: one CTA per SM, fewer when there cannot be that many tiles
     int64_t grid = (p.N / kTok + (p.N < p.E ? p.N : p.E)) * p.n_wt;
     if (grid > num_sms) grid = num_sms;
-    return launch_pdl(gemm_mx4_kernel<kDual, kTok>, dim3((unsigned)grid), dim3(kThreads), C::kSmem, st, tx, tw0, tw1,
-                      p);
+    return launch_pdl(gemm_mx4_kernel<kDual, kTok>, dim3((unsigned)grid), dim3(C::kThreads), C::kSmem, st, tx, txs, tw0,
+                      tw1, p);
 }
 
 }  // namespace mx4
@@ -518,8 +546,8 @@ cudaError_t launch_grouped_mx4(const mx4::Args& p, cudaStream_t st, int num_sms)
     using namespace mx4;
     // few rows per expert: narrow token tiles leave room for twice the stages, i.e. the weights in flight
     const bool few = p.N <= (int64_t)48 * p.E;
-    if (p.qb) return few ? launch<true, 64>(p, st, num_sms) : launch<true, 224>(p, st, num_sms);
-    return few ? launch<false, 64>(p, st, num_sms) : launch<false, 224>(p, st, num_sms);
+    if (p.qb) return few ? launch<true, 64>(p, st, num_sms) : launch<true, 208>(p, st, num_sms);
+    return few ? launch<false, 64>(p, st, num_sms) : launch<false, 208>(p, st, num_sms);
 }
 
 }  // namespace jmoe

@@ -28,6 +28,7 @@ struct Args {
     int K;                 // reduction length
     int M;                 // weight rows per expert and matrix
     int n_wt;              // weight tiles per expert (set by the launcher)
+    int vec_scales;        // rows of scales are whole 32-byte pieces on 32-byte boundaries (set by the launcher)
     int band_max;          // token tiles per L2 band, at most (set by the launcher)
 };
 
