@@ -980,6 +980,7 @@ int jamba_moe_grouped_mx4(const uint8_t* xq, const uint8_t* xs, const int32_t* o
     p.E = n_experts;
     p.reset_status = 1;
     p.N = N;
+    p.rows = N;
     p.xq = xq;
     p.xs = xs;
     p.qa = Q;
@@ -1061,6 +1062,7 @@ int jamba_moe_forward_mx4(const uint16_t* x, const float* router_W, const float*
     p.count = hdr->counts;
     p.E = kExperts;
     p.N = L.rows_cap;
+    p.rows = TK;
     p.xq = xq;
     p.xs = xs;
     p.qa = Q1;

@@ -47,26 +47,29 @@ constexpr int kEpiWarps = 8;
 constexpr int kSfStages = 4;      // stages whose scales a lane holds: 32 bytes of each of its rows
 constexpr uint32_t kMaxPolls = 1u << 22;  // ~0.3 s of polling: far above any healthy wait
 
-template <int kTok>
+// kPair: two CTAs work on one tile of 256 weight rows.
+template <bool kPair, int kTok>
 struct Cfg {
-    static constexpr int kSfBlocks = (kTok + 127) / 128;  // 512-byte blocks of token scales per 128 k
+    static constexpr int kCtas = kPair ? 2 : 1;
+    static constexpr int kTokCta = kTok / kCtas;            // token rows whose codes a CTA holds
+    static constexpr int kSfBlocks = (kTok + 127) / 128;    // 512-byte blocks of token scales per 128 k
     static constexpr int kA = kWRows * kStageBytes;
-    static constexpr int kB = kTok * kStageBytes;
+    static constexpr int kB = kTokCta * kStageBytes;
     static constexpr int kSfA = 2 * 512;
     static constexpr int kSfB = 2 * kSfBlocks * 512;
     static constexpr int kStage = kA + kB + kSfA + kSfB;
     static constexpr int kStages = (227 * 1024 - 8 * 1024) / kStage;
     static constexpr int kSfCols = 8 + 8 * kSfBlocks;
     static constexpr int kSfCol0 = 2 * kTok;
-    static constexpr uint32_t kTmemCols = kSfCol0 + kStages * kSfCols <= 256 ? 256 : 512;
+    static constexpr int kSfSets = (512 - kSfCol0) / kSfCols < kStages ? (512 - kSfCol0) / kSfCols : kStages;
+    static constexpr uint32_t kTmemCols = kSfCol0 + kSfSets * kSfCols <= 256 ? 256 : 512;
     static constexpr int kSfWarps = 1 + kSfBlocks;
     static constexpr int kEpiWarp0 = 2 + kSfWarps;
     static constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
     static constexpr int kBars = 2 * kStages + 5;
     static constexpr int kSmem = kStages * kStage + 1024 + 8 * kBars;
     static_assert(kThreads >= kMaxGroups, "one thread per group");
-    static_assert(kTok % 16 == 0 && kB % 1024 == 0 && kStages >= 3, "tile");
-    static_assert(kSfCol0 + kStages * kSfCols <= 512, "TMEM");
+    static_assert(kTok % 16 == 0 && kB % 1024 == 0 && kStages >= 3 && kSfSets >= 2, "tile");
 };
 
 struct Tile {
@@ -125,12 +128,13 @@ __device__ __forceinline__ void ld_scales(const uint8_t* ptr, bool vec, int word
     }
 }
 
-template <bool kDual, int kTok>
-__global__ void __launch_bounds__(Cfg<kTok>::kThreads, 1)
+template <bool kDual, bool kPair, int kTok>
+__global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
     gemm_mx4_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXs,
                     const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUtensorMap tmW1, Args p) {
-    using C = Cfg<kTok>;
+    using C = Cfg<kPair, kTok>;
     constexpr int kStages = C::kStages, kEpiWarp0 = C::kEpiWarp0;
+    constexpr int kRowsCta = kDual ? kWRows / 2 : kWRows;  // weight rows (of each matrix) of a CTA's part of a tile
     extern __shared__ uint8_t smem_raw[];
     __shared__ Groups G;
     __shared__ int warp_sum[C::kThreads / 32];
@@ -169,7 +173,9 @@ __global__ void __launch_bounds__(Cfg<kTok>::kThreads, 1)
         __syncthreads();
     }
     const int total = G.tile0[p.E];
-    if ((int)blockIdx.x >= total) return;  // no tile for this CTA: nothing was taken yet
+    const int rank = kPair ? (int)tc::cluster_rank() : 0;                      // 0: the CTA that issues the MMAs
+    const int first = (int)blockIdx.x / C::kCtas, stride = (int)gridDim.x / C::kCtas;  // this CTA's tiles
+    if (first >= total) return;  // no tile for this CTA (or pair): nothing was taken yet
 
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;                          // [kStages][128 rows][128 B]
@@ -180,16 +186,16 @@ __global__ void __launch_bounds__(Cfg<kTok>::kThreads, 1)
     uint64_t* empty = full + kStages;            // [kStages] MMAs reading the stage are done
     uint64_t* acc_full = empty + kStages;        // [2] accumulator complete
     uint64_t* acc_empty = acc_full + 2;          // [2] accumulator read out by the epilogue
-    uint64_t* mma_done = acc_empty + 2;          // every issued MMA complete (teardown)
+    uint64_t* mma_done = acc_empty + 2;          // every issued MMA complete (after an abort)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            tc::mbar_init(&full[s], 1 + C::kSfWarps);
+            tc::mbar_init(&full[s], 1 + C::kCtas * C::kSfWarps);
             tc::mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             tc::mbar_init(&acc_full[b], 1);
-            tc::mbar_init(&acc_empty[b], kEpiWarps);
+            tc::mbar_init(&acc_empty[b], C::kCtas * kEpiWarps);
         }
         tc::mbar_init(mma_done, 1);
         abort_flag = 0;
@@ -201,9 +207,15 @@ __global__ void __launch_bounds__(Cfg<kTok>::kThreads, 1)
         tc::prefetch_tmap(&tmW0);
         if (kDual) tc::prefetch_tmap(&tmW1);
     }
-    if (warp == 1) tc::tmem_alloc(&tmem_holder, C::kTmemCols);
+    if (warp == 1) {
+        if constexpr (kPair)
+            tc::tmem_alloc_pair(&tmem_holder, C::kTmemCols);
+        else
+            tc::tmem_alloc(&tmem_holder, C::kTmemCols);
+    }
     tc::tc_fence_before();
     __syncthreads();
+    if constexpr (kPair) tc::cluster_sync();  // the peer's barriers are there before anything arrives on them
     tc::tc_fence_after();
     const uint32_t tmem = tmem_holder;
     const int KW = p.K / 128;          // 4-byte words of scales per row
@@ -214,18 +226,29 @@ __global__ void __launch_bounds__(Cfg<kTok>::kThreads, 1)
         if (!abort_flag) fail(p.hdr, &abort_flag);
         return false;
     };
+    // Arrive on the barrier of the CTA that issues the MMAs.  What it then starts in this CTA (its tensor core
+    // reading this CTA's scales, or overwriting the accumulator) is ordered after this thread's own proxy or tcgen05 fence.
+    auto arrive = [&](uint64_t* bar) {
+        if constexpr (kPair)
+            tc::mbar_arrive_cluster(tc::map_to_cta(tc::smem_u32(bar), 0));
+        else
+            tc::mbar_arrive(bar);
+    };
 
     if (warp == 0) {
-        // ---------------- codes
+        // ---------------- codes: this CTA's weight rows and its half (kPair) of the token rows; the first CTA's
+        // barrier counts the bytes of both
         int g = 0;
         bool ok = true;
         Tile t;
-        for (int L = blockIdx.x; ok && L < total; L += gridDim.x) {
+        for (int L = first; ok && L < total; L += stride) {
             tile_at<kTok>(G, p, L, t);
-            const int w_row0 = t.e * p.M + t.n * (kDual ? kWRows / 2 : kWRows);
+            const int w_row0 = t.e * p.M + (t.n * C::kCtas + rank) * kRowsCta;
+            const int part = ((t.ntok + 15) & ~15) / C::kCtas;  // this CTA's token rows
+            const int x_row0 = (int)t.row0 + rank * part;
             // one copy for a tile (nearly) full of tokens, else the 32-row boxes it needs
-            const int n_box = t.ntok > kTok / kBoxRows * kBoxRows - kBoxRows ? 0 : (t.ntok + kBoxRows - 1) / kBoxRows;
-            const uint32_t bytes = C::kA + (n_box == 0 ? kTok : n_box * kBoxRows) * kStageBytes;
+            const int n_box = part > C::kTokCta / kBoxRows * kBoxRows ? 0 : (part + kBoxRows - 1) / kBoxRows;
+            const uint32_t bytes = C::kCtas * (C::kA + (n_box == 0 ? C::kTokCta : n_box * kBoxRows) * kStageBytes);
             for (int kb = 0; kb < KB; ++kb, ++g) {
                 const int s = g % kStages, r = g / kStages;
                 if (r > 0 && !(ok = wait(&empty[s], r - 1))) break;
@@ -233,35 +256,43 @@ __global__ void __launch_bounds__(Cfg<kTok>::kThreads, 1)
                 uint8_t* db = sB + s * C::kB;
                 const int x = kb * kStageBytes;
                 if (tc::elect_one()) {
-                    tc::mbar_arrive_expect_tx(&full[s], bytes);
+                    if (rank == 0) tc::mbar_arrive_expect_tx(&full[s], bytes);
+                    auto load = [&](uint8_t* dst, const CUtensorMap* tm, int row) {
+                        if constexpr (kPair)
+                            tc::tma_load_2d_pair(dst, tm, tc::map_to_cta(tc::smem_u32(&full[s]), 0), x, row);
+                        else
+                            tc::tma_load_2d(dst, tm, &full[s], x, row);
+                    };
                     if (kDual) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            tc::tma_load_2d(da + q * 32 * kStageBytes, &tmW0, &full[s], x, w_row0 + 16 * q);
-                            tc::tma_load_2d(da + (q * 32 + 16) * kStageBytes, &tmW1, &full[s], x, w_row0 + 16 * q);
+                            load(da + q * 32 * kStageBytes, &tmW0, w_row0 + 16 * q);
+                            load(da + (q * 32 + 16) * kStageBytes, &tmW1, w_row0 + 16 * q);
                         }
                     } else {
-                        tc::tma_load_2d(da, &tmW0, &full[s], x, w_row0);
+                        load(da, &tmW0, w_row0);
                     }
-                    if (n_box == 0) tc::tma_load_2d(db, &tmX, &full[s], x, (int)t.row0);
+                    if (n_box == 0) load(db, &tmX, x_row0);
                     for (int i = 0; i < n_box; ++i)
-                        tc::tma_load_2d(db + i * kBoxRows * kStageBytes, &tmXs, &full[s], x,
-                                        (int)t.row0 + i * kBoxRows);
+                        load(db + i * kBoxRows * kStageBytes, &tmXs, x_row0 + i * kBoxRows);
                 }
                 __syncwarp();
                 issued = g + 1;
             }
         }
+        // the last stages' arrivals come from the other CTA: they have to be here before this one may end
+        if (kPair)
+            for (int s = 0; ok && s < kStages && s < g; ++s) ok = wait(&empty[s], (g - 1 - s) / kStages);
     } else if (warp < kEpiWarp0 && warp >= 2) {
         // ---------------- scales: warp 2 those of the weights, each other warp 128 token rows
         const int blk = warp - 3;
-        const int64_t stride = p.K / 32;
+        const int64_t row_bytes = p.K / 32;
         const uint32_t dst0 = tc::smem_u32(blk < 0 ? sSA : sSB + 512 * blk) + 16 * lane;
         const uint32_t dst_stage = blk < 0 ? C::kSfA : C::kSfB;
         const uint32_t dst_word = blk < 0 ? 512 : 512 * C::kSfBlocks;
         // what is loaded next: rows 32 i + lane (i < live) of tile L, from stage kb on
         const uint8_t* ptr[4] = {};
-        int L = blockIdx.x, kb = 0, live = 0;
+        int L = first, kb = 0, live = 0;
         auto open_tile = [&]() {
             Tile t;
             tile_at<kTok>(G, p, L, t);
@@ -272,11 +303,11 @@ __global__ void __launch_bounds__(Cfg<kTok>::kThreads, 1)
                 const int r = 32 * i + lane;
                 // rows past the expert's (or the matrix's) last: any valid row, their results are not stored
                 if (blk < 0) {
-                    const int j = kDual ? t.n * 64 + 16 * i + (lane & 15) : t.n * kWRows + r;
-                    ptr[i] = (kDual && lane >= 16 ? p.sb : p.sa) + ((int64_t)t.e * p.M + min(j, p.M - 1)) * stride;
+                    const int j = (t.n * C::kCtas + rank) * kRowsCta + (kDual ? 16 * i + (lane & 15) : r);
+                    ptr[i] = (kDual && lane >= 16 ? p.sb : p.sa) + ((int64_t)t.e * p.M + min(j, p.M - 1)) * row_bytes;
                 } else {
                     const int64_t row = t.row0 + 128 * blk + r;
-                    ptr[i] = p.xs + (row < p.N ? row : p.N - 1) * stride;
+                    ptr[i] = p.xs + (row < p.N ? row : p.N - 1) * row_bytes;
                 }
             }
         };
@@ -290,7 +321,7 @@ __global__ void __launch_bounds__(Cfg<kTok>::kThreads, 1)
             kb += kSfStages;
             if (kb >= KB) {
                 kb = 0;
-                L += gridDim.x;
+                L += stride;
             }
             return n;
         };
@@ -313,7 +344,7 @@ __global__ void __launch_bounds__(Cfg<kTok>::kThreads, 1)
                                  : "memory");
                 tc::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&full[s]);
+                if (lane == 0) arrive(&full[s]);
                 ++g;
             }
 #pragma unroll
@@ -322,63 +353,73 @@ __global__ void __launch_bounds__(Cfg<kTok>::kThreads, 1)
                 for (int j = 0; j < 2 * kSfStages; ++j) cur[i][j] = nxt[i][j];
             n = n_next;
         }
-    } else if (warp == 1) {
+    } else if (warp == 1 && rank == 0) {
         // ---------------- MMA issuer: the warp stays converged, one elected lane issues
         const uint64_t adesc0 = tc::sw128_kmajor_desc(tc::smem_u32(sA)), bdesc0 = tc::sw128_kmajor_desc(tc::smem_u32(sB));
         const uint64_t sadesc0 = tc::linear_desc(tc::smem_u32(sSA)), sbdesc0 = tc::linear_desc(tc::smem_u32(sSB));
+        auto commit = [](uint64_t* bar) {
+            if constexpr (kPair)
+                tc::mma_commit_pair(bar);
+            else
+                tc::mma_commit(bar);
+        };
         int g = 0, it = 0;
         bool ok = true;
         Tile t;
-        for (int L = blockIdx.x; L < total; L += gridDim.x, ++it) {
+        for (int L = first; L < total; L += stride, ++it) {
             tile_at<kTok>(G, p, L, t);
             const int n_mma = (t.ntok + 15) & ~15;
-            const uint32_t idesc0 = tc::idesc_mx4_f32(kWRows, n_mma, 0);
-            const uint32_t idesc2 = tc::idesc_mx4_f32(kWRows, n_mma, 2);
+            const uint32_t idesc0 = tc::idesc_mx4_f32(C::kCtas * kWRows, n_mma, 0);
+            const uint32_t idesc2 = tc::idesc_mx4_f32(C::kCtas * kWRows, n_mma, 2);
             const int b = it & 1, u = it >> 1;
             if (u > 0 && !(ok = wait(&acc_empty[b], u - 1))) break;
             const uint32_t d_tmem = tmem + (uint32_t)(b * kTok);
             for (int kb = 0; kb < KB; ++kb, ++g) {
                 const int s = g % kStages, r = g / kStages;
                 if (!(ok = wait(&full[s], r))) break;
+                // fewer sets of scale columns than stages: the MMAs that read this set last have to be done
+                if (C::kSfSets < kStages && g >= C::kSfSets &&
+                    !(ok = wait(&empty[(g - C::kSfSets) % kStages], (g - C::kSfSets) / kStages)))
+                    break;
                 tc::tc_fence_after();
                 if (tc::elect_one()) {
-                    const uint32_t sf = tmem + C::kSfCol0 + (uint32_t)(s * C::kSfCols);
+                    const uint32_t sf = tmem + C::kSfCol0 + (uint32_t)(g % C::kSfSets * C::kSfCols);
                     const uint64_t adesc = adesc0 + (uint32_t)(s * (C::kA >> 4)), bdesc = bdesc0 + (uint32_t)(s * (C::kB >> 4));
                     const uint64_t sadesc = sadesc0 + (uint32_t)(s * (C::kSfA >> 4));
                     const uint64_t sbdesc = sbdesc0 + (uint32_t)(s * (C::kSfB >> 4));
                     // 512 bytes = +32 in a descriptor's address field; the second 128 k of a last stage need not be there
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
-                        tc::tmem_cp_32x16(sf + 4 * w, sadesc + 32 * w);
+                        tc::tmem_cp_32x16<kPair>(sf + 4 * w, sadesc + 32 * w);
 #pragma unroll
                         for (int i = 0; i < C::kSfBlocks; ++i)
-                            tc::tmem_cp_32x16(sf + 8 + 4 * (C::kSfBlocks * w + i), sbdesc + 32 * (C::kSfBlocks * w + i));
+                            tc::tmem_cp_32x16<kPair>(sf + 8 + 4 * (C::kSfBlocks * w + i), sbdesc + 32 * (C::kSfBlocks * w + i));
                     }
                     // 64 k = 32 bytes of the 128-byte row = +2 in the address field
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
                         if (w == 0 || 2 * kb + 1 < KW) {
                             const uint32_t sfa = sf + 4 * w, sfb = sf + 8 + 4 * C::kSfBlocks * w;
-                            tc::mma_mx4_ss(d_tmem, adesc + 4 * w, bdesc + 4 * w, idesc0, sfa, sfb, (kb | w) != 0);
-                            tc::mma_mx4_ss(d_tmem, adesc + 4 * w + 2, bdesc + 4 * w + 2, idesc2, sfa, sfb, 1);
+                            tc::mma_mx4_ss<kPair>(d_tmem, adesc + 4 * w, bdesc + 4 * w, idesc0, sfa, sfb, (kb | w) != 0);
+                            tc::mma_mx4_ss<kPair>(d_tmem, adesc + 4 * w + 2, bdesc + 4 * w + 2, idesc2, sfa, sfb, 1);
                         }
                     }
-                    tc::mma_commit(&empty[s]);
-                    if (kb == KB - 1) tc::mma_commit(&acc_full[b]);
+                    commit(&empty[s]);
+                    if (kb == KB - 1) commit(&acc_full[b]);
                 }
                 __syncwarp();
                 issued = g + 1;
             }
             if (!ok) break;
         }
-        if (tc::elect_one()) tc::mma_commit(mma_done);  // arrives once every MMA issued above has completed
+        if (!ok && tc::elect_one()) commit(mma_done);  // arrives once every MMA issued above has completed
         __syncwarp();
-    } else {
+    } else if (warp >= kEpiWarp0) {
         // ---------------- epilogue
         const int qd = warp & 3, part = (warp - kEpiWarp0) >> 2;
         int it = 0;
         Tile t;
-        for (int L = blockIdx.x; L < total; L += gridDim.x, ++it) {
+        for (int L = first; L < total; L += stride, ++it) {
             tile_at<kTok>(G, p, L, t);
             const int b = it & 1, u = it >> 1;
             const bool ok = wait(&acc_full[b], u);
@@ -389,7 +430,7 @@ __global__ void __launch_bounds__(Cfg<kTok>::kThreads, 1)
             auto release = [&]() {
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&acc_empty[b]);
+                if (lane == 0) arrive(&acc_empty[b]);
                 released = true;
             };
 #pragma unroll 1
@@ -401,7 +442,7 @@ __global__ void __launch_bounds__(Cfg<kTok>::kThreads, 1)
                 if constexpr (kDual) {
                     // lanes < 16 keep the gate of tokens c .. c+15 and take the up values from lane + 16;
                     // lanes >= 16 keep the up of tokens c+16 .. c+31 and take the gate values from lane - 16
-                    const int j = t.n * 64 + 16 * qd + (lane & 15);
+                    const int j = (t.n * C::kCtas + rank) * kRowsCta + 16 * qd + (lane & 15);
                     const int tok0 = c + ((lane < 16) ? 0 : 16);
                     uint16_t* hcol = p.y16 + (t.row0 + tok0) * p.M + j;
 #pragma unroll
@@ -415,7 +456,7 @@ __global__ void __launch_bounds__(Cfg<kTok>::kThreads, 1)
                             hcol[(int64_t)i * p.M] = f32_to_bf16_bits(silu_fast(gt) * up);
                     }
                 } else {
-                    const int j = t.n * kWRows + 32 * qd + lane;
+                    const int j = (t.n * C::kCtas + rank) * kRowsCta + 32 * qd + lane;
                     if (p.wts) {
                         const int32_t a_l = c + lane < t.ntok ? p.perm[t.row0 + c + lane] : -1;
                         const float w_l = a_l >= 0 ? p.wts[a_l] : 0.0f;
@@ -461,23 +502,27 @@ __global__ void __launch_bounds__(Cfg<kTok>::kThreads, 1)
     tc::tc_fence_before();
     __syncthreads();
     if (abort_flag) {
-        if (warp == 0 && lane == 0) {
+        if (warp == 0 && lane == 0 && rank == 0) {
             for (int s = 0; s < kStages; ++s) {
                 if (s >= issued) continue;
                 const int last = (issued - 1 - s) / kStages;
                 // a copy of round r completes phase `last` of full[s] once the scales are there too, else this wait runs out
-                for (uint32_t i = 0; i < kMaxPolls && !tc::mbar_try_wait(&full[s], last & 1); ++i)
-                    __nanosleep(64);
+                for (uint32_t i = 0; i < kMaxPolls && !tc::mbar_try_wait(&full[s], last & 1); ++i) __nanosleep(64);
             }
         }
-        if (warp == 1 && lane == 0 && issued > 0) {
+        if (warp == 1 && lane == 0) {  // completes if the issuer gave up; if it did not, its last MMAs are long done after this
             for (uint32_t i = 0; i < kMaxPolls && !tc::mbar_try_wait(mma_done, 0); ++i) __nanosleep(64);
         }
         __syncthreads();
     }
+    // nothing of the pair's is still on its way into the other CTA's shared or tensor memory
+    if constexpr (kPair) tc::cluster_sync();
     if (warp == 1) {
         tc::tc_fence_after();
-        tc::tmem_dealloc(tmem, C::kTmemCols);
+        if constexpr (kPair)
+            tc::tmem_dealloc_pair(tmem, C::kTmemCols);
+        else
+            tc::tmem_dealloc(tmem, C::kTmemCols);
     }
 }
 
@@ -512,20 +557,20 @@ bool make_map(CUtensorMap* m, const uint8_t* ptr, uint64_t rows, uint64_t row_by
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kDual, int kTok>
+template <bool kDual, bool kPair, int kTok>
 cudaError_t launch(Args p, cudaStream_t st, int num_sms) {
-    using C = Cfg<kTok>;
+    using C = Cfg<kPair, kTok>;
     CUtensorMap tx, txs, tw0, tw1;
     const uint64_t row_bytes = (uint64_t)p.K / 2, w_rows = (uint64_t)p.E * p.M;
     constexpr uint32_t kWBox = kDual ? 16 : kWRows;
-    if (!make_map(&tx, p.xq, (uint64_t)p.N, row_bytes, kTok) ||
+    if (!make_map(&tx, p.xq, (uint64_t)p.N, row_bytes, C::kTokCta) ||
         !make_map(&txs, p.xq, (uint64_t)p.N, row_bytes, kBoxRows) || !make_map(&tw0, p.qa, w_rows, row_bytes, kWBox) ||
         !make_map(&tw1, kDual ? p.qb : p.qa, w_rows, row_bytes, kWBox))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(gemm_mx4_kernel<kDual, kTok>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         C::kSmem);
+    const auto kernel = gemm_mx4_kernel<kDual, kPair, kTok>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    constexpr int kRows = kDual ? kWRows / 2 : kWRows;
+    constexpr int kRows = C::kCtas * (kDual ? kWRows / 2 : kWRows);
     p.n_wt = (p.M + kRows - 1) / kRows;
     const uintptr_t scales = reinterpret_cast<uintptr_t>(p.xs) | reinterpret_cast<uintptr_t>(p.sa) |
                              reinterpret_cast<uintptr_t>(kDual ? p.sb : p.sa);
@@ -534,20 +579,33 @@ cudaError_t launch(Args p, cudaStream_t st, int num_sms) {
     const int64_t per_tile = (int64_t)kTok * (p.K / 2);
     p.band_max = (int)(per_tile >= (32ll << 20) ? 1 : (32ll << 20) / per_tile);
     // persistent: one CTA per SM, fewer when there cannot be that many tiles
-    int64_t grid = (p.N / kTok + (p.N < p.E ? p.N : p.E)) * p.n_wt;
-    if (grid > num_sms) grid = num_sms;
-    return launch_pdl(gemm_mx4_kernel<kDual, kTok>, dim3((unsigned)grid), dim3(C::kThreads), C::kSmem, st, tx, txs, tw0,
-                      tw1, p);
+    int64_t tiles = (p.rows / kTok + (p.rows < p.E ? p.rows : p.E)) * p.n_wt;
+    if (tiles > num_sms / C::kCtas) tiles = num_sms / C::kCtas;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)tiles * C::kCtas);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C::kCtas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = kPair ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, tx, txs, tw0, tw1, p);
 }
 
 }  // namespace mx4
 
 cudaError_t launch_grouped_mx4(const mx4::Args& p, cudaStream_t st, int num_sms) {
     using namespace mx4;
-    // few rows per expert: narrow token tiles leave room for twice the stages, i.e. the weights in flight
-    const bool few = p.N <= (int64_t)48 * p.E;
-    if (p.qb) return few ? launch<true, 64>(p, st, num_sms) : launch<true, 208>(p, st, num_sms);
-    return few ? launch<false, 64>(p, st, num_sms) : launch<false, 208>(p, st, num_sms);
+    // few rows per expert: single CTAs with narrow token tiles, whose stages are the weights in flight
+    const bool few = p.rows <= (int64_t)48 * p.E;
+    if (p.qb) return few ? launch<true, false, 64>(p, st, num_sms) : launch<true, true, 208>(p, st, num_sms);
+    return few ? launch<false, false, 64>(p, st, num_sms) : launch<false, true, 208>(p, st, num_sms);
 }
 
 }  // namespace jmoe

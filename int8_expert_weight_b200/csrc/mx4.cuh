@@ -15,6 +15,7 @@ struct Args {
     int E;                 // experts
     int reset_status;      // this call owns the status word: clear it, and report a bad group table there
     int64_t N;             // rows of x
+    int64_t rows;          // of them at most in groups
     const uint8_t* xq;     // x codes [N][K / 2] and scales [N][K / 32]
     const uint8_t* xs;
     const uint8_t* qa;     // weights W (dual: W1) codes [E][M][K / 2] and scales [E][M][K / 32]
