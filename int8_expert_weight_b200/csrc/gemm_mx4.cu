@@ -18,7 +18,7 @@
 // Persistent, one CTA per SM, warps in roles; a pipeline stage holds 256 of K (128 bytes of codes per row):
 //   warp 0      codes: TMA boxes of 128 bytes x 128 (dual: 16) weight rows and x 32 token rows, SWIZZLE_128B
 //   warp 1      TMEM allocator; per stage copies the scales to TMEM (tcgen05.cp) and issues 4 MMAs of 64 k
-//   2-3 warps   scales: one warp per 128 rows of weights or tokens.  The tensor core wants 512-byte blocks of 128 rows
+//   4-6 warps   scales: two sets, in turns, of one warp per 128 rows of weights or tokens.  The tensor core wants 512-byte blocks of 128 rows
 //               x 128 k with row r at 16 (r % 32) + 4 (r / 32); a lane reads 32 bytes (a DRAM sector: 1024 of
 //               K, four stages) of rows lane, lane + 32, + 64, + 96 into registers, four stages ahead and across
 //               tiles, and stores 16 bytes per block.  (4-byte copies per row and 128 k fetched each sector
@@ -63,8 +63,8 @@ struct Cfg {
     static constexpr int kSfCol0 = 2 * kTok;
     static constexpr int kSfSets = (512 - kSfCol0) / kSfCols < kStages ? (512 - kSfCol0) / kSfCols : kStages;
     static constexpr uint32_t kTmemCols = kSfCol0 + kSfSets * kSfCols <= 256 ? 256 : 512;
-    static constexpr int kSfWarps = 1 + kSfBlocks;
-    static constexpr int kEpiWarp0 = 2 + kSfWarps;
+    static constexpr int kSfWarps = 1 + kSfBlocks;          // of one set of scale warps
+    static constexpr int kEpiWarp0 = 2 + 2 * kSfWarps;
     static constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
     static constexpr int kBars = 2 * kStages + 5;
     static constexpr int kSmem = kStages * kStage + 1024 + 8 * kBars;
@@ -73,7 +73,7 @@ struct Cfg {
 };
 
 struct Tile {
-    int e, n;      // expert, weight tile
+    int e = 0, n;  // expert, weight tile
     int64_t row0;  // first row of the token tile
     int ntok;      // its rows (1 .. kTok)
 };
@@ -85,23 +85,25 @@ struct Groups {
     int row0[kMaxGroups];
 };
 
+// Tile L.  t.e is where the search starts: the group of an earlier tile (the role's last one), or 0.
 template <int kTok>
 __device__ __forceinline__ void tile_at(const Groups& G, const Args& p, int L, Tile& t) {
-    int e = 0;  // the last group whose first tile is <= L: groups without rows have no tile
-#pragma unroll
-    for (int s = kMaxGroups / 2; s > 0; s >>= 1)
-        if (e + s < p.E && G.tile0[e + s] <= L) e += s;
-    const int count = G.count[e], local = L - G.tile0[e];
-    const int nt = (count + kTok - 1) / kTok;
-    const int nb = (nt + p.band_max - 1) / p.band_max;
-    const int bfull = (nt + nb - 1) / nb;
-    const int band = local / (bfull * p.n_wt);
-    const int m_first = band * bfull;
-    const int bsz = min(bfull, nt - m_first);
-    const int within = local - band * bfull * p.n_wt;
-    const int m = m_first + within % bsz;
+    int e = t.e;  // to the last group whose first tile is <= L: groups without rows have no tile
+    while (e + 1 < p.E && G.tile0[e + 1] <= L) ++e;
+    const int count = G.count[e], nt = (count + kTok - 1) / kTok;
+    int within = L - G.tile0[e], m_first = 0, bsz = nt;
+    if (nt > p.band_max) {  // more token tiles than a band holds: bands as even as possible
+        const int nb = (nt + p.band_max - 1) / p.band_max;
+        const int bfull = (nt + nb - 1) / nb;
+        const int band = within / (bfull * p.n_wt);
+        within -= band * bfull * p.n_wt;
+        m_first = band * bfull;
+        bsz = min(bfull, nt - m_first);
+    }
+    const int n = within / bsz;
+    const int m = m_first + within - n * bsz;
     t.e = e;
-    t.n = within / bsz;
+    t.n = n;
     t.row0 = (int64_t)G.row0[e] + m * kTok;
     t.ntok = min(kTok, count - m * kTok);
 }
@@ -284,18 +286,20 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
         if (kPair)
             for (int s = 0; ok && s < kStages && s < g; ++s) ok = wait(&empty[s], (g - 1 - s) / kStages);
     } else if (warp < kEpiWarp0 && warp >= 2) {
-        // ---------------- scales: warp 2 those of the weights, each other warp 128 token rows
-        const int blk = warp - 3;
+        // ---------------- scales: two sets of warps take turns by kSfStages stages; the first warp of a set takes the
+        // weights' scales, each other one those of 128 token rows
+        const int set = (warp - 2) / C::kSfWarps, blk = (warp - 2) % C::kSfWarps - 1;
         const int64_t row_bytes = p.K / 32;
         const uint32_t dst0 = tc::smem_u32(blk < 0 ? sSA : sSB + 512 * blk) + 16 * lane;
         const uint32_t dst_stage = blk < 0 ? C::kSfA : C::kSfB;
         const uint32_t dst_word = blk < 0 ? 512 : 512 * C::kSfBlocks;
-        // what is loaded next: rows 32 i + lane (i < live) of tile L, from stage kb on
+        // what is loaded next: rows 32 i + lane (i < live) of tile L, from the tile's stage kb, this CTA's stage g_load, on
         const uint8_t* ptr[4] = {};
-        int L = first, kb = 0, live = 0;
+        int L = first, kb = 0, g_load = 0, live = 0, opened = -1;
+        Tile t;
         auto open_tile = [&]() {
-            Tile t;
             tile_at<kTok>(G, p, L, t);
+            opened = L;
             const int n_mma = (t.ntok + 15) & ~15;
             live = blk < 0 ? 4 : max(0, min(4, (n_mma - 128 * blk + 31) / 32));
 #pragma unroll
@@ -311,29 +315,37 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
                 }
             }
         };
-        auto fetch = [&](uint32_t (&v)[4][2 * kSfStages]) -> int {  // returns the stages held (0: past the last tile)
-            if (L >= total) return 0;
-            if (kb == 0) open_tile();
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < live) ld_scales(ptr[i] + 8 * kb, p.vec_scales, KW - 2 * kb, v[i]);
-            const int n = min(kSfStages, KB - kb);
+        auto skip = [&]() {
+            g_load += min(kSfStages, KB - kb);
             kb += kSfStages;
             if (kb >= KB) {
                 kb = 0;
                 L += stride;
             }
+        };
+        // Loads this set's next stages; returns how many (0: past the last tile), `at`: the first one.
+        auto fetch = [&](uint32_t (&v)[4][2 * kSfStages], int& at) -> int {
+            if (L >= total) return 0;
+            if (opened != L) open_tile();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < live) ld_scales(ptr[i] + 8 * kb, p.vec_scales, KW - 2 * kb, v[i]);
+            at = g_load;
+            const int n = min(kSfStages, KB - kb);
+            skip();
+            if (L < total) skip();
             return n;
         };
         uint32_t cur[4][2 * kSfStages] = {}, nxt[4][2 * kSfStages] = {};
-        int g = 0;
+        if (set == 1) skip();
+        int g = 0, g_next = 0;
         bool ok = true;
-        for (int n = fetch(cur); ok && n > 0;) {
-            const int n_next = fetch(nxt);
+        for (int n = fetch(cur, g); ok && n > 0;) {
+            const int n_next = fetch(nxt, g_next);
 #pragma unroll
             for (int st = 0; st < kSfStages; ++st) {
                 if (st >= n) break;
-                const int s = g % kStages, r = g / kStages;
+                const int s = (g + st) % kStages, r = (g + st) / kStages;
                 const bool free_ = r == 0 || wait(&empty[s], r - 1);
                 if (!(ok = __all_sync(0xffffffffu, free_))) break;
 #pragma unroll
@@ -345,13 +357,13 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) arrive(&full[s]);
-                ++g;
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < 2 * kSfStages; ++j) cur[i][j] = nxt[i][j];
             n = n_next;
+            g = g_next;
         }
     } else if (warp == 1 && rank == 0) {
         // ---------------- MMA issuer: the warp stays converged, one elected lane issues
