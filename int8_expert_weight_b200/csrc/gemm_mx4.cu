@@ -44,6 +44,8 @@ constexpr int kWRows = 128;
 constexpr int kStageBytes = 128;  // bytes of codes per row and stage: 256 of K
 constexpr int kBoxRows = 32;      // token rows per copy
 constexpr int kEpiWarps = 8;
+constexpr int kOutPitch = 80;     // bytes per token of a warp's 16-token staging area (32 bf16, plus 16: no bank conflicts)
+constexpr int kOutBytes = 16 * kOutPitch;
 constexpr int kSfStages = 4;      // stages whose scales a lane holds: 32 bytes of each of its rows
 constexpr uint32_t kMaxPolls = 1u << 22;  // ~0.3 s of polling: far above any healthy wait
 
@@ -58,7 +60,7 @@ struct Cfg {
     static constexpr int kSfA = 2 * 512;
     static constexpr int kSfB = 2 * kSfBlocks * 512;
     static constexpr int kStage = kA + kB + kSfA + kSfB;
-    static constexpr int kStages = (227 * 1024 - 8 * 1024) / kStage;
+    static constexpr int kStages = (227 * 1024 - 6 * 1024 - kEpiWarps * kOutBytes) / kStage;
     static constexpr int kSfCols = 8 + 8 * kSfBlocks;
     static constexpr int kSfCol0 = 2 * kTok;
     static constexpr int kSfSets = (512 - kSfCol0) / kSfCols < kStages ? (512 - kSfCol0) / kSfCols : kStages;
@@ -67,7 +69,7 @@ struct Cfg {
     static constexpr int kEpiWarp0 = 2 + 2 * kSfWarps;
     static constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
     static constexpr int kBars = 2 * kStages + 5;
-    static constexpr int kSmem = kStages * kStage + 1024 + 8 * kBars;
+    static constexpr int kSmem = kStages * kStage + kEpiWarps * kOutBytes + 1024 + 8 * kBars;
     static_assert(kThreads >= kMaxGroups, "one thread per group");
     static_assert(kTok % 16 == 0 && kB % 1024 == 0 && kStages >= 3 && kSfSets >= 2, "tile");
 };
@@ -111,6 +113,14 @@ __device__ __forceinline__ void tile_at(const Groups& G, const Args& p, int L, T
 // SiLU with the fast exponential and division intrinsics: a few fp32 ulps from the exact value,
 // far below the bf16 rounding of h that follows.
 __device__ __forceinline__ float silu_fast(float a) { return __fdividef(a, 1.0f + __expf(-a)); }
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ uint32_t pack_bf16(uint32_t lo, uint32_t hi) {  // fp32 bits
+    return pack_bf16(__uint_as_float(lo), __uint_as_float(hi));
+}
 
 __device__ __forceinline__ void fail(WsHeader* hdr, volatile int* abort) {
     *abort = 1;
@@ -184,7 +194,8 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
     uint8_t* sB = sA + kStages * C::kA;          // [kStages][kTok rows][128 B]
     uint8_t* sSA = sB + kStages * C::kB;         // [kStages][2][512 B]
     uint8_t* sSB = sSA + kStages * C::kSfA;      // [kStages][2][kSfBlocks][512 B]
-    uint64_t* full = reinterpret_cast<uint64_t*>(sSB + kStages * C::kSfB);  // [kStages] codes and scales are there
+    uint8_t* sOut = sSB + kStages * C::kSfB;     // [kEpiWarps][16 tokens][kOutPitch]
+    uint64_t* full = reinterpret_cast<uint64_t*>(sOut + kEpiWarps * kOutBytes);  // [kStages] codes and scales are there
     uint64_t* empty = full + kStages;            // [kStages] MMAs reading the stage are done
     uint64_t* acc_full = empty + kStages;        // [2] accumulator complete
     uint64_t* acc_empty = acc_full + 2;          // [2] accumulator read out by the epilogue
@@ -445,30 +456,79 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
                 if (lane == 0) arrive(&acc_empty[b]);
                 released = true;
             };
+            const int j0 = (t.n * C::kCtas + rank) * kRowsCta + (kDual ? 16 : 32) * qd;  // this warp's first column of y
+            if (kDual || p.y16) {
+                // bf16: fragments of 16 lanes x 8 tokens go through shared memory (transposed, 16 tokens at a time) and
+                // leave as 16-byte pieces of y rows; rows whose length is no multiple of 8 element by element.
+                // (Trading values between neighbouring lanes and storing 4 bytes each took 2300 cycles per 32 tokens.)
+                // dual: gate and up of one j are in lanes l and l + 16, so in the same place of the two fragments.
+                constexpr int kPitch = kDual ? 48 : kOutPitch, kJ = kDual ? 16 : 32;
+                const uint32_t out = tc::smem_u32(sOut + (warp - kEpiWarp0) * kOutBytes);
+                // where this lane's matrix column goes: dual has 2 j blocks x 2 token blocks a matrix store, plain 4 x 1
+                const uint32_t st = out + (kDual ? (8 * (lane >> 4) + (lane & 7)) * kPitch + 16 * ((lane >> 3) & 1)
+                                                 : (lane & 7) * kPitch + 16 * (lane >> 3));
 #pragma unroll 1
-            for (int c = 32 * part; c < t.ntok; c += 64) {
-                uint32_t v[32];
-                tc::tmem_ld32(t_lane + (uint32_t)c, v);
-                tc::tmem_wait_ld();
-                if (c + 64 >= t.ntok) release();
-                if constexpr (kDual) {
-                    // lanes < 16 keep the gate of tokens c .. c+15 and take the up values from lane + 16;
-                    // lanes >= 16 keep the up of tokens c+16 .. c+31 and take the gate values from lane - 16
-                    const int j = (t.n * C::kCtas + rank) * kRowsCta + 16 * qd + (lane & 15);
-                    const int tok0 = c + ((lane < 16) ? 0 : 16);
-                    uint16_t* hcol = p.y16 + (t.row0 + tok0) * p.M + j;
+                for (int c = 32 * part; c < t.ntok; c += 64) {
+                    uint32_t lo[16], hi[16];  // TMEM lanes 0-15 and 16-31 of the quarter
+                    tc::tmem_ld_16x32(t_lane + (uint32_t)c, lo);
+                    tc::tmem_ld_16x32(t_lane + (16u << 16) + (uint32_t)c, hi);
+                    tc::tmem_wait_ld();
+                    if (c + 64 >= t.ntok) release();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float own_keep = __uint_as_float(v[(lane < 16) ? i : 16 + i]);
-                        const float own_send = __uint_as_float(v[(lane < 16) ? 16 + i : i]);
-                        const float other = __shfl_xor_sync(0xffffffffu, own_send, 16);
-                        const float gt = (lane < 16) ? own_keep : other;
-                        const float up = (lane < 16) ? other : own_keep;
-                        if (tok0 + i < t.ntok && j < p.M)
-                            hcol[(int64_t)i * p.M] = f32_to_bf16_bits(silu_fast(gt) * up);
+                    for (int half = 0; half < 2; ++half) {
+                        const int tok0 = c + 16 * half;
+                        if (tok0 >= t.ntok) break;
+                        if constexpr (kDual) {
+                            uint32_t m[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int k = 8 * half + 2 * i;
+                                m[i] = pack_bf16(silu_fast(__uint_as_float(lo[k])) * __uint_as_float(hi[k]),
+                                                 silu_fast(__uint_as_float(lo[k + 1])) * __uint_as_float(hi[k + 1]));
+                            }
+                            tc::stmatrix_x4_trans(st, m[0], m[1], m[2], m[3]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const int k = 8 * half + 4 * i;
+                                tc::stmatrix_x4_trans(st + 8 * i * kPitch, pack_bf16(lo[k], lo[k + 1]),
+                                                      pack_bf16(lo[k + 2], lo[k + 3]), pack_bf16(hi[k], hi[k + 1]),
+                                                      pack_bf16(hi[k + 2], hi[k + 3]));
+                            }
+                        }
+                        __syncwarp();
+                        uint16_t* y = p.y16 + (t.row0 + tok0) * p.M + j0;
+                        if (p.M % 8 == 0) {
+                            constexpr int kParts = kJ / 8, kToks = 32 / kParts;  // 16-byte pieces of a row; rows per store
+#pragma unroll
+                            for (int i = 0; i < 16 / kToks; ++i) {
+                                const int tok = kToks * i + lane / kParts, j = 8 * (lane % kParts);
+                                uint4 v;
+                                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                             : "r"(out + tok * kPitch + 2 * j)
+                                             : "memory");
+                                if (tok0 + tok < t.ntok && j0 + j < p.M)
+                                    *reinterpret_cast<uint4*>(y + (int64_t)tok * p.M + j) = v;
+                            }
+                        } else {
+                            for (int tok = 0; tok < 16 && tok0 + tok < t.ntok; ++tok) {
+                                uint16_t v;
+                                asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(out + tok * kPitch + 2 * (lane % kJ)) : "memory");
+                                if (lane < kJ && j0 + lane < p.M) y[(int64_t)tok * p.M + lane] = v;
+                            }
+                        }
+                        __syncwarp();  // the area is rewritten by the next 16 tokens
                     }
-                } else {
-                    const int j = (t.n * C::kCtas + rank) * kRowsCta + 32 * qd + lane;
+                }
+            } else {
+                const int j = j0 + lane;
+#pragma unroll 1
+                for (int c = 32 * part; c < t.ntok; c += 64) {
+                    uint32_t v[32];
+                    tc::tmem_ld32(t_lane + (uint32_t)c, v);
+                    tc::tmem_wait_ld();
+                    if (c + 64 >= t.ntok) release();
                     if (p.wts) {
                         const int32_t a_l = c + lane < t.ntok ? p.perm[t.row0 + c + lane] : -1;
                         const float w_l = a_l >= 0 ? p.wts[a_l] : 0.0f;
@@ -478,30 +538,11 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
                             const float wt = __shfl_sync(0xffffffffu, w_l, i);
                             if (a >= 0 && j < p.M) p.y32[(int64_t)a * p.M + j] = wt * __uint_as_float(v[i]);
                         }
-                    } else if (p.y32) {
+                    } else {
                         float* ycol = p.y32 + (t.row0 + c) * p.M + j;
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (c + i < t.ntok && j < p.M) ycol[(int64_t)i * p.M] = __uint_as_float(v[i]);
-                    } else if (p.M & 1) {  // bf16 rows of odd length: no pair of them starts on 4 bytes throughout
-                        uint16_t* ycol = p.y16 + (t.row0 + c) * p.M + j;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (c + i < t.ntok && j < p.M) ycol[(int64_t)i * p.M] = f32_to_bf16_bits(__uint_as_float(v[i]));
-                    } else {
-                        // neighbouring lanes trade: the even one stores columns j, j + 1 of even tokens, the odd one
-                        // columns j - 1, j of odd tokens, 4 bytes each
-                        const int odd = lane & 1;
-                        uint16_t* ycol = p.y16 + (t.row0 + c + odd) * p.M + (j - odd);
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            const float keep = __uint_as_float(odd ? v[i + 1] : v[i]);
-                            const float other = __shfl_xor_sync(0xffffffffu, __uint_as_float(odd ? v[i] : v[i + 1]), 1);
-                            const uint32_t lo = f32_to_bf16_bits(odd ? other : keep);
-                            const uint32_t hi = f32_to_bf16_bits(odd ? keep : other);
-                            if (c + i + odd < t.ntok && j < p.M)
-                                *reinterpret_cast<uint32_t*>(ycol + (int64_t)i * p.M) = lo | (hi << 16);
-                        }
                     }
                 }
             }
