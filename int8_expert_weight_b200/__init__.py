@@ -158,6 +158,14 @@ def _one_device(ref: torch.Tensor, **tensors) -> torch.device:
     return ref.device
 
 
+def _launch(fn, dev: torch.device, stream: Optional[torch.cuda.Stream], *args) -> int:
+    """fn(*args, stream) with `dev` current; the switch is left out when it is already (it costs over a microsecond)."""
+    if torch.cuda.current_device() == dev.index:
+        return fn(*args, _stream_ptr(stream, dev))
+    with torch.cuda.device(dev):
+        return fn(*args, _stream_ptr(stream, dev))
+
+
 def jamba_moe_status_string(status: int) -> str:
     return load_library().jamba_moe_status_string(int(status)).decode()
 
@@ -347,16 +355,14 @@ def jamba_moe_quantize_mx4(W: torch.Tensor, stream: Optional[torch.cuda.Stream] 
     n_mats = W.numel() // (rows * cols) if W.numel() else 0
     q_shape, s_shape = W.shape[:-1] + (cols // 2,), W.shape[:-1] + (cols // 32,)
     if out is None:
-        Q = torch.empty(q_shape, dtype=torch.uint8, device=W.device)
-        S = torch.empty(s_shape, dtype=torch.uint8, device=W.device)
+        Q = W.new_empty(q_shape, dtype=torch.uint8)
+        S = W.new_empty(s_shape, dtype=torch.uint8)
     else:
         Q, S = out
         _check(Q, "Q", torch.uint8, q_shape)
         _check(S, "S", torch.uint8, s_shape)
     dev = _one_device(W, Q=Q, S=S)
-    with torch.cuda.device(dev):
-        st = lib.jamba_moe_quantize_mx4(W.data_ptr(), n_mats, rows, cols, Q.data_ptr(), S.data_ptr(),
-                                        _stream_ptr(stream, dev))
+    st = _launch(lib.jamba_moe_quantize_mx4, dev, stream, W.data_ptr(), n_mats, rows, cols, Q.data_ptr(), S.data_ptr())
     if st != 0:
         raise JmoeError(st, "jamba_moe_quantize_mx4")
     return Q, S
@@ -375,12 +381,12 @@ def jamba_moe_dequantize_mx4(Q: torch.Tensor, S: torch.Tensor, out: Optional[tor
     n_mats = Q.numel() // (rows * (cols // 2)) if Q.numel() else 0
     w_shape = Q.shape[:-1] + (cols,)
     if out is None:
-        out = torch.empty(w_shape, dtype=torch.bfloat16, device=Q.device)
-    _check(out, "out", torch.bfloat16, w_shape)
+        out = Q.new_empty(w_shape, dtype=torch.bfloat16)
+    else:
+        _check(out, "out", torch.bfloat16, w_shape)
     dev = _one_device(Q, S=S, out=out)
-    with torch.cuda.device(dev):
-        st = lib.jamba_moe_dequantize_mx4(Q.data_ptr(), S.data_ptr(), n_mats, rows, cols, out.data_ptr(),
-                                          _stream_ptr(stream, dev))
+    st = _launch(lib.jamba_moe_dequantize_mx4, dev, stream, Q.data_ptr(), S.data_ptr(), n_mats, rows, cols,
+                 out.data_ptr())
     if st != 0:
         raise JmoeError(st, "jamba_moe_dequantize_mx4")
     return out
@@ -414,20 +420,20 @@ def jamba_moe_grouped_mx4(xq: torch.Tensor, xs: torch.Tensor, offsets: torch.Ten
     _check(S, "S", torch.uint8, (E, rows, cols // 32))
     _check(offsets, "offsets", torch.int32, (E + 1,))
     if y is None:
-        y = torch.empty((N, rows), dtype=out_dtype, device=xq.device)
-    _check(y, "y", out_dtype, (N, rows))
+        y = xq.new_empty((N, rows), dtype=out_dtype)
+    else:
+        _check(y, "y", out_dtype, (N, rows))
     need = jamba_moe_grouped_mx4_workspace_size(N, rows, cols, E)
     if need == 0:
         raise JmoeError(2, "jamba_moe_grouped_mx4_workspace_size")
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=xq.device)
-    _check(workspace, "workspace", torch.uint8)
+        workspace = xq.new_empty(need)
+    else:
+        _check(workspace, "workspace", torch.uint8)
     dev = _one_device(xq, xs=xs, offsets=offsets, Q=Q, S=S, y=y, workspace=workspace)
-    with torch.cuda.device(dev):
-        st = lib.jamba_moe_grouped_mx4(xq.data_ptr(), xs.data_ptr(), offsets.data_ptr(), N, rows, cols, E,
-                                       Q.data_ptr(), S.data_ptr(), y.data_ptr(),
-                                       OUT_BF16 if out_dtype == torch.bfloat16 else OUT_FP32, workspace.data_ptr(),
-                                       workspace.numel(), _stream_ptr(stream, dev))
+    st = _launch(lib.jamba_moe_grouped_mx4, dev, stream, xq.data_ptr(), xs.data_ptr(), offsets.data_ptr(), N, rows, cols,
+                 E, Q.data_ptr(), S.data_ptr(), y.data_ptr(), OUT_BF16 if out_dtype == torch.bfloat16 else OUT_FP32,
+                 workspace.data_ptr(), workspace.numel())
     if st != 0:
         raise JmoeError(st, "jamba_moe_grouped_mx4")
     return y
@@ -462,28 +468,30 @@ def jamba_moe_forward_mx4(x: torch.Tensor, router_W: torch.Tensor, router_bias: 
     _check(S3, "S3", torch.uint8, (E, ffn, d // 32))
     _check(S2, "S2", torch.uint8, (E, d, ffn // 32))
     if y is None:
-        y = torch.empty((T, d), dtype=torch.bfloat16, device=x.device)
-    _check(y, "y", torch.bfloat16, (T, d))
+        y = x.new_empty((T, d))
+    else:
+        _check(y, "y", torch.bfloat16, (T, d))
     if topk_ids is None:
-        topk_ids = torch.empty((T, TOP_K), dtype=torch.int32, device=x.device)
+        topk_ids = x.new_empty((T, TOP_K), dtype=torch.int32)
+    else:
+        _check(topk_ids, "topk_ids", torch.int32, (T, TOP_K))
     if topk_w is None:
-        topk_w = torch.empty((T, TOP_K), dtype=torch.float32, device=x.device)
-    _check(topk_ids, "topk_ids", torch.int32, (T, TOP_K))
-    _check(topk_w, "topk_w", torch.float32, (T, TOP_K))
+        topk_w = x.new_empty((T, TOP_K), dtype=torch.float32)
+    else:
+        _check(topk_w, "topk_w", torch.float32, (T, TOP_K))
     need = jamba_moe_workspace_size_mx4(T, d, ffn, E, TOP_K)
     if need == 0:
         raise JmoeError(2, "jamba_moe_workspace_size_mx4")
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    _check(workspace, "workspace", torch.uint8)
+        workspace = x.new_empty(need, dtype=torch.uint8)
+    else:
+        _check(workspace, "workspace", torch.uint8)
     p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
     dev = _one_device(x, router_W=router_W, router_bias=router_bias, Q1=Q1, S1=S1, Q3=Q3, S3=S3, Q2=Q2, S2=S2, y=y,
                       topk_ids=topk_ids, topk_w=topk_w, workspace=workspace)
-    with torch.cuda.device(dev):
-        st = lib.jamba_moe_forward_mx4(x.data_ptr(), router_W.data_ptr(), p(router_bias), Q1.data_ptr(),
-                                       S1.data_ptr(), Q3.data_ptr(), S3.data_ptr(), Q2.data_ptr(), S2.data_ptr(), T, d,
-                                       ffn, E, TOP_K, y.data_ptr(), p(topk_ids), p(topk_w), workspace.data_ptr(),
-                                       workspace.numel(), _stream_ptr(stream, dev))
+    st = _launch(lib.jamba_moe_forward_mx4, dev, stream, x.data_ptr(), router_W.data_ptr(), p(router_bias),
+                 Q1.data_ptr(), S1.data_ptr(), Q3.data_ptr(), S3.data_ptr(), Q2.data_ptr(), S2.data_ptr(), T, d, ffn, E,
+                 TOP_K, y.data_ptr(), topk_ids.data_ptr(), topk_w.data_ptr(), workspace.data_ptr(), workspace.numel())
     if st != 0:
         raise JmoeError(st, "jamba_moe_forward_mx4")
     return y, topk_ids, topk_w

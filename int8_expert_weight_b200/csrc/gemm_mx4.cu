@@ -34,6 +34,8 @@
 // each weight tile.  Tile i of a CTA is its index + i * grid.
 #include <cuda.h>
 
+#include <atomic>
+
 #include "mx4.cuh"
 #include "tc.cuh"
 
@@ -155,6 +157,7 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
     pdl_wait();
+    pdl_trigger();  // the next kernel's CTAs may take their places beside this one's; they wait for its end
     // ---- group table: thread e takes group e
     {
         const int e = threadIdx.x;
@@ -551,7 +554,6 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
     }
 
     // ---- teardown: after an abort, let in-flight copies and MMAs finish (bounded) before TMEM goes
-    pdl_trigger();
     tc::tc_fence_before();
     __syncthreads();
     if (abort_flag) {
@@ -617,12 +619,21 @@ cudaError_t launch(Args p, cudaStream_t st, int num_sms) {
     const uint64_t row_bytes = (uint64_t)p.K / 2, w_rows = (uint64_t)p.E * p.M;
     constexpr uint32_t kWBox = kDual ? 16 : kWRows;
     if (!make_map(&tx, p.xq, (uint64_t)p.N, row_bytes, C::kTokCta) ||
-        !make_map(&txs, p.xq, (uint64_t)p.N, row_bytes, kBoxRows) || !make_map(&tw0, p.qa, w_rows, row_bytes, kWBox) ||
-        !make_map(&tw1, kDual ? p.qb : p.qa, w_rows, row_bytes, kWBox))
+        !make_map(&txs, p.xq, (uint64_t)p.N, row_bytes, kBoxRows) || !make_map(&tw0, p.qa, w_rows, row_bytes, kWBox))
         return cudaErrorInvalidValue;
+    tw1 = tw0;
+    if (kDual && !make_map(&tw1, p.qb, w_rows, row_bytes, kWBox)) return cudaErrorInvalidValue;
     const auto kernel = gemm_mx4_kernel<kDual, kPair, kTok>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    static std::atomic<uint64_t> ready{0};  // devices whose kernel has its shared-memory limit raised
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (!bit || !(ready.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
     constexpr int kRows = C::kCtas * (kDual ? kWRows / 2 : kWRows);
     p.n_wt = (p.M + kRows - 1) / kRows;
     const uintptr_t scales = reinterpret_cast<uintptr_t>(p.xs) | reinterpret_cast<uintptr_t>(p.sa) |
