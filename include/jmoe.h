@@ -212,8 +212,7 @@ int jamba_moe_dequantize_mx4(const uint8_t* Q, const uint8_t* S, int64_t n_mats,
  *   xq, xs:  codes uint8 [N][cols / 2], scales uint8 [N][cols / 32] of the rows, grouped by expert
  *   offsets: int32 [n_experts + 1], on the device, 0 <= offsets[0] <= ... <= offsets[n_experts] <= N.
  *            An expert may have no row; its weights are then not read.  Offsets that break the rule are
- *            reported as JMOE_DEV_BAD_INDEX in the workspace status word; no access leaves the
- *            arrays, and y is then not valid.
+ *            reported as JMOE_DEV_BAD_INDEX in the workspace status word, and y is left as it was.
  *   Q, S:    codes uint8 [n_experts][rows][cols / 2], scales uint8 [n_experts][rows][cols / 32]
  *   y:       [N][rows], bf16 (out_type JMOE_OUT_BF16) or fp32 (JMOE_OUT_FP32).  Rows that belong to no
  *            expert are left as they were.

@@ -129,6 +129,73 @@ __device__ __forceinline__ void fail(WsHeader* hdr, volatile int* abort) {
     set_status(hdr, JMOE_DEV_TIMEOUT);
 }
 
+// 16 tokens (the first n of them live) of a warp's 32 TMEM lanes as bf16, y rows row0 .., columns j0 ..: the fragments
+// v (see tmem_ld_16x16; lanes 0-15, then 16-31) go transposed through the warp's area `out` of shared memory and
+// leave as 16-byte pieces of y rows, element by element where rows are no multiple of 8 long.  (Trading values
+// between neighbouring lanes and storing 4 bytes each took 1200 cycles per 16 tokens.)
+// kDual: gate and up of one j are in lanes l and l + 16, so in the same place of the two halves of v.
+template <bool kDual>
+__device__ __forceinline__ void store_bf16(const Args& p, uint32_t out, const uint32_t (&v)[16], int64_t row0, int n, int j0,
+                                           int lane) {
+    constexpr int kPitch = kDual ? 48 : kOutPitch, kJ = kDual ? 16 : 32;
+    if constexpr (kDual) {  // 2 j blocks x 2 token blocks of 8
+        uint32_t m[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            m[i] = pack_bf16(silu_fast(__uint_as_float(v[2 * i])) * __uint_as_float(v[8 + 2 * i]),
+                             silu_fast(__uint_as_float(v[2 * i + 1])) * __uint_as_float(v[9 + 2 * i]));
+        tc::stmatrix_x4_trans(out + (8 * (lane >> 4) + (lane & 7)) * kPitch + 16 * ((lane >> 3) & 1), m[0], m[1], m[2], m[3]);
+    } else {  // 4 j blocks, for each of two token blocks
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            tc::stmatrix_x4_trans(out + (8 * i + (lane & 7)) * kPitch + 16 * (lane >> 3), pack_bf16(v[4 * i], v[4 * i + 1]),
+                                  pack_bf16(v[4 * i + 2], v[4 * i + 3]), pack_bf16(v[8 + 4 * i], v[9 + 4 * i]),
+                                  pack_bf16(v[10 + 4 * i], v[11 + 4 * i]));
+    }
+    __syncwarp();
+    uint16_t* y = p.y16 + row0 * p.M + j0;
+    if (p.M % 8 == 0) {
+        constexpr int kParts = kJ / 8, kToks = 32 / kParts;  // 16-byte pieces of a row; rows per store
+#pragma unroll
+        for (int i = 0; i < 16 / kToks; ++i) {
+            const int tok = kToks * i + lane / kParts, j = 8 * (lane % kParts);
+            uint4 q;
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                         : "r"(out + tok * kPitch + 2 * j)
+                         : "memory");
+            if (tok < n && j0 + j < p.M) *reinterpret_cast<uint4*>(y + (int64_t)tok * p.M + j) = q;
+        }
+    } else {
+        for (int tok = 0; tok < 16 && tok < n; ++tok) {
+            uint16_t q;
+            asm volatile("ld.shared.b16 %0, [%1];" : "=h"(q) : "r"(out + tok * kPitch + 2 * (lane % kJ)) : "memory");
+            if (lane < kJ && j0 + lane < p.M) y[(int64_t)tok * p.M + lane] = q;
+        }
+    }
+    __syncwarp();  // the area is rewritten by the next 16 tokens
+}
+
+// 16 tokens (the first n of them live) of column j as fp32: y rows row0 .., or, times their routing weights, the slots of
+// their assignments.
+__device__ __forceinline__ void store_fp32(const Args& p, const uint32_t (&v)[16], int64_t row0, int n, int j, int lane) {
+    if (p.wts) {
+        const int32_t a_l = lane < min(n, 16) ? p.perm[row0 + lane] : -1;
+        const float w_l = a_l >= 0 ? p.wts[a_l] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int32_t a = __shfl_sync(0xffffffffu, a_l, i);
+            const float wt = __shfl_sync(0xffffffffu, w_l, i);
+            if (a >= 0 && j < p.M) p.y32[(int64_t)a * p.M + j] = wt * __uint_as_float(v[i]);
+        }
+    } else {
+        float* y = p.y32 + row0 * p.M + j;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (i < n && j < p.M) y[(int64_t)i * p.M] = __uint_as_float(v[i]);
+    }
+}
+
 // 32 bytes of scales; `vec`: 32-byte aligned and whole, else `words` 4-byte words of them are there.
 __device__ __forceinline__ void ld_scales(const uint8_t* ptr, bool vec, int words, uint32_t (&v)[2 * kSfStages]) {
     if (vec) {
@@ -169,10 +236,9 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
             G.count[e] = count;
             G.row0[e] = (int)row0;
         }
-        if (p.reset_status && blockIdx.x == 0) {
-            bad = __syncthreads_or(bad);
-            if (e == 0) p.hdr->status = bad ? JMOE_DEV_BAD_INDEX : JMOE_OK;
-        }
+        bad = __syncthreads_or(bad);
+        if (p.reset_status && blockIdx.x == 0 && e == 0) p.hdr->status = bad ? JMOE_DEV_BAD_INDEX : JMOE_OK;
+        if (bad) return;  // from here on the groups are in order and apart
         const int tiles = (count + kTok - 1) / kTok * p.n_wt;
         int sum = tiles;
 #pragma unroll
@@ -441,8 +507,9 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
         if (!ok && tc::elect_one()) commit(mma_done);  // arrives once every MMA issued above has completed
         __syncwarp();
     } else if (warp >= kEpiWarp0) {
-        // ---------------- epilogue
-        const int qd = warp & 3, part = (warp - kEpiWarp0) >> 2;
+        // ---------------- epilogue, 16 tokens at a time
+        const int qd = warp & 3, ew = warp - kEpiWarp0, part = ew >> 2;
+        const bool bf16 = kDual || p.y16;
         int it = 0;
         Tile t;
         for (int L = first; L < total; L += stride, ++it) {
@@ -452,104 +519,37 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
             if (!__all_sync(0xffffffffu, ok)) break;  // tcgen05.ld below is warp-collective
             tc::tc_fence_after();
             const uint32_t t_lane = tmem + ((uint32_t)(32 * qd) << 16) + (uint32_t)(b * kTok);
-            bool released = false;
+            const int n_unit = (t.ntok + 15) / 16;  // this warp's: part, part + 2, ...
             auto release = [&]() {
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive(&acc_empty[b]);
-                released = true;
+            };
+            // bf16: two fragments (16 lanes x 8 tokens) of TMEM lanes 0-15 and two of lanes 16-31 of the quarter;
+            // fp32: 16 tokens of this thread's lane
+            auto load = [&](int unit, uint32_t (&v)[16]) {
+                if (bf16) {
+                    tc::tmem_ld_16x16(t_lane + (uint32_t)(16 * unit), v);
+                    tc::tmem_ld_16x16(t_lane + (16u << 16) + (uint32_t)(16 * unit), v + 8);
+                } else {
+                    tc::tmem_ld16(t_lane + (uint32_t)(16 * unit), v);
+                }
+                tc::tmem_wait_ld();
             };
             const int j0 = (t.n * C::kCtas + rank) * kRowsCta + (kDual ? 16 : 32) * qd;  // this warp's first column of y
-            if (kDual || p.y16) {
-                // bf16: fragments of 16 lanes x 8 tokens go through shared memory (transposed, 16 tokens at a time) and
-                // leave as 16-byte pieces of y rows; rows whose length is no multiple of 8 element by element.
-                // (Trading values between neighbouring lanes and storing 4 bytes each took 2300 cycles per 32 tokens.)
-                // dual: gate and up of one j are in lanes l and l + 16, so in the same place of the two fragments.
-                constexpr int kPitch = kDual ? 48 : kOutPitch, kJ = kDual ? 16 : 32;
-                const uint32_t out = tc::smem_u32(sOut + (warp - kEpiWarp0) * kOutBytes);
-                // where this lane's matrix column goes: dual has 2 j blocks x 2 token blocks a matrix store, plain 4 x 1
-                const uint32_t st = out + (kDual ? (8 * (lane >> 4) + (lane & 7)) * kPitch + 16 * ((lane >> 3) & 1)
-                                                 : (lane & 7) * kPitch + 16 * (lane >> 3));
-#pragma unroll 1
-                for (int c = 32 * part; c < t.ntok; c += 64) {
-                    uint32_t lo[16], hi[16];  // TMEM lanes 0-15 and 16-31 of the quarter
-                    tc::tmem_ld_16x32(t_lane + (uint32_t)c, lo);
-                    tc::tmem_ld_16x32(t_lane + (16u << 16) + (uint32_t)c, hi);
-                    tc::tmem_wait_ld();
-                    if (c + 64 >= t.ntok) release();
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int tok0 = c + 16 * half;
-                        if (tok0 >= t.ntok) break;
-                        if constexpr (kDual) {
-                            uint32_t m[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int k = 8 * half + 2 * i;
-                                m[i] = pack_bf16(silu_fast(__uint_as_float(lo[k])) * __uint_as_float(hi[k]),
-                                                 silu_fast(__uint_as_float(lo[k + 1])) * __uint_as_float(hi[k + 1]));
-                            }
-                            tc::stmatrix_x4_trans(st, m[0], m[1], m[2], m[3]);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int k = 8 * half + 4 * i;
-                                tc::stmatrix_x4_trans(st + 8 * i * kPitch, pack_bf16(lo[k], lo[k + 1]),
-                                                      pack_bf16(lo[k + 2], lo[k + 3]), pack_bf16(hi[k], hi[k + 1]),
-                                                      pack_bf16(hi[k + 2], hi[k + 3]));
-                            }
-                        }
-                        __syncwarp();
-                        uint16_t* y = p.y16 + (t.row0 + tok0) * p.M + j0;
-                        if (p.M % 8 == 0) {
-                            constexpr int kParts = kJ / 8, kToks = 32 / kParts;  // 16-byte pieces of a row; rows per store
-#pragma unroll
-                            for (int i = 0; i < 16 / kToks; ++i) {
-                                const int tok = kToks * i + lane / kParts, j = 8 * (lane % kParts);
-                                uint4 v;
-                                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                                             : "r"(out + tok * kPitch + 2 * j)
-                                             : "memory");
-                                if (tok0 + tok < t.ntok && j0 + j < p.M)
-                                    *reinterpret_cast<uint4*>(y + (int64_t)tok * p.M + j) = v;
-                            }
-                        } else {
-                            for (int tok = 0; tok < 16 && tok0 + tok < t.ntok; ++tok) {
-                                uint16_t v;
-                                asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(out + tok * kPitch + 2 * (lane % kJ)) : "memory");
-                                if (lane < kJ && j0 + lane < p.M) y[(int64_t)tok * p.M + lane] = v;
-                            }
-                        }
-                        __syncwarp();  // the area is rewritten by the next 16 tokens
-                    }
-                }
-            } else {
-                const int j = j0 + lane;
-#pragma unroll 1
-                for (int c = 32 * part; c < t.ntok; c += 64) {
-                    uint32_t v[32];
-                    tc::tmem_ld32(t_lane + (uint32_t)c, v);
-                    tc::tmem_wait_ld();
-                    if (c + 64 >= t.ntok) release();
-                    if (p.wts) {
-                        const int32_t a_l = c + lane < t.ntok ? p.perm[t.row0 + c + lane] : -1;
-                        const float w_l = a_l >= 0 ? p.wts[a_l] : 0.0f;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int32_t a = __shfl_sync(0xffffffffu, a_l, i);
-                            const float wt = __shfl_sync(0xffffffffu, w_l, i);
-                            if (a >= 0 && j < p.M) p.y32[(int64_t)a * p.M + j] = wt * __uint_as_float(v[i]);
-                        }
-                    } else {
-                        float* ycol = p.y32 + (t.row0 + c) * p.M + j;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (c + i < t.ntok && j < p.M) ycol[(int64_t)i * p.M] = __uint_as_float(v[i]);
-                    }
-                }
+            auto store = [&](int unit, const uint32_t (&v)[16]) {
+                if (bf16)
+                    store_bf16<kDual>(p, tc::smem_u32(sOut + ew * kOutBytes), v, t.row0 + 16 * unit, t.ntok - 16 * unit, j0, lane);
+                else
+                    store_fp32(p, v, t.row0 + 16 * unit, t.ntok - 16 * unit, j0 + lane, lane);
+            };
+            uint32_t v[16];
+            for (int unit = part; unit < n_unit; unit += 2) {
+                load(unit, v);
+                if (unit + 2 >= n_unit) release();
+                store(unit, v);
             }
-            if (!released) release();  // a warp whose columns hold no tokens of this tile
+            if (part >= n_unit) release();  // a warp whose columns hold no tokens of this tile
         }
     }
 

@@ -33,14 +33,15 @@ struct Args {
     int band_max;          // token tiles per L2 band, at most (set by the launcher)
 };
 
-// Rows of expert e.  Whatever the table holds, [row0, row0 + count) lies inside the N rows of x and y.
-// Returns whether its entries break the rule 0 <= begin, count >= 0, begin + count <= N.
+// Rows of expert e.  Returns whether its entries break the rule 0 <= begin, 0 <= count, begin + count <= N; as offsets
+// (count NULL) that all keep it are in ascending order.
 __device__ __forceinline__ bool group_at(const Args& p, int e, int64_t& row0, int& count) {
     const int64_t b = p.begin[e];
     const int64_t c = p.count ? p.count[e] : p.begin[e + 1] - b;
-    row0 = b < 0 ? 0 : (b > p.N ? p.N : b);
-    count = (int)(c < 0 ? 0 : (c > p.N - row0 ? p.N - row0 : c));
-    return b != row0 || c != count;
+    const bool bad = b < 0 || c < 0 || b + c > p.N;
+    row0 = bad ? 0 : b;
+    count = bad ? 0 : (int)c;
+    return bad;
 }
 
 }  // namespace mx4
