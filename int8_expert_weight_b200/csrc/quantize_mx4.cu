@@ -12,8 +12,8 @@
 // correctly rounded code: no residual check as for the int8 and E4M3 codes is needed.
 //
 // HBM-bound: 2 bytes read and 17/32 written per element (and the reverse).  Blocks never straddle
-// rows (cols is a multiple of 32), so both kernels walk the matrices as one flat run of 8-element
-// chunks: a thread reads 16 bytes, four neighbouring lanes hold a block.
+// rows (cols is a multiple of 32), so both kernels walk the matrices as one flat run of 16-element
+// chunks: two neighbouring lanes hold a block, a thread reads (quantization) or writes 32 bytes at a time.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -22,6 +22,34 @@ namespace jmoe {
 
 constexpr int kMxThreads = 256;
 constexpr int kMxUnroll = 4;  // chunks a thread has in flight
+
+// 16 bf16 values; kWide: on a 32-byte boundary, else on a 16-byte one.  Each is read or written once.
+struct Chunk {
+    uint4 a, b;
+};
+template <bool kWide>
+__device__ __forceinline__ Chunk ld_chunk(const uint16_t* p) {
+    Chunk c;
+    if constexpr (kWide)
+        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(c.a.x), "=r"(c.a.y), "=r"(c.a.z), "=r"(c.a.w), "=r"(c.b.x), "=r"(c.b.y), "=r"(c.b.z),
+                       "=r"(c.b.w)
+                     : "l"(p));
+    else
+        c = Chunk{ld_stream_v4(p), ld_stream_v4(p + 8)};
+    return c;
+}
+template <bool kWide>
+__device__ __forceinline__ void st_chunk(uint16_t* p, const uint32_t (&o)[8]) {
+    if constexpr (kWide) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(o[0]), "r"(o[1]), "r"(o[2]),
+                     "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(p)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        reinterpret_cast<uint4*>(p)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+}
 
 // Largest magnitude (bf16 bits) of the 8 values of a chunk.
 __device__ __forceinline__ uint32_t chunk_amax(const uint4& v) {
@@ -66,26 +94,28 @@ __device__ __forceinline__ uint32_t block_amax(uint32_t a) {
     return max(a, __shfl_xor_sync(0xffffffffu, a, 2));
 }
 
+template <bool kWide>
 __global__ void __launch_bounds__(kMxThreads) quantize_mx4_kernel(const uint16_t* __restrict__ W, int64_t chunks,
                                                                   uint8_t* __restrict__ Q, uint8_t* __restrict__ S) {
     pdl_wait();
     pdl_trigger();
     const int64_t step = (int64_t)gridDim.x * kMxThreads;
-    // every lane of a warp takes part in the shuffles; chunks is a multiple of 4, so whole blocks are live
+    // every lane of a warp takes part in the shuffles; chunks is a multiple of 2, so whole blocks are live
     for (int64_t c0 = (int64_t)blockIdx.x * kMxThreads; c0 < chunks; c0 += kMxUnroll * step) {
-        uint4 v[kMxUnroll];
+        Chunk v[kMxUnroll];
 #pragma unroll
         for (int u = 0; u < kMxUnroll; ++u) {
             const int64_t c = c0 + u * step + threadIdx.x;
-            v[u] = c < chunks ? ld_stream_v4(W + c * 8) : make_uint4(0, 0, 0, 0);
+            v[u] = c < chunks ? ld_chunk<kWide>(W + c * 16) : Chunk{};
         }
 #pragma unroll
         for (int u = 0; u < kMxUnroll; ++u) {
             const int64_t c = c0 + u * step + threadIdx.x;
-            const uint32_t s = mx_scale(block_amax(chunk_amax(v[u])));
+            const uint32_t m = max(chunk_amax(v[u].a), chunk_amax(v[u].b));
+            const uint32_t s = mx_scale(max(m, __shfl_xor_sync(0xffffffffu, m, 1)));
             if (c >= chunks) continue;
-            *reinterpret_cast<uint32_t*>(Q + c * 4) = mx_codes(v[u], s);
-            if ((c & 3) == 0) S[c >> 2] = (uint8_t)s;
+            *reinterpret_cast<uint2*>(Q + c * 8) = make_uint2(mx_codes(v[u].a, s), mx_codes(v[u].b, s));
+            if ((c & 1) == 0) S[c >> 1] = (uint8_t)s;
         }
     }
 }
@@ -117,8 +147,27 @@ __global__ void __launch_bounds__(kMxThreads)
     }
 }
 
+// Values of 8 codes times `scale` as bf16 pairs.
+__device__ __forceinline__ void mx_values(uint32_t q, float scale, uint32_t* o) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(q));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+        o[i] = (uint32_t)f32_to_bf16_bits(f.x * scale) | ((uint32_t)f32_to_bf16_bits(f.y * scale) << 16);
+    }
+}
+
 // The inverse: code x scale as bf16, exact (an E2M1 number has two significant bits, and the least
 // magnitude, 2^-128, is a bf16 subnormal); products beyond bf16's range become infinities, a scale byte of 255 NaN.
+template <bool kWide>
 __global__ void __launch_bounds__(kMxThreads) dequantize_mx4_kernel(const uint8_t* __restrict__ Q,
                                                                     const uint8_t* __restrict__ S, int64_t chunks,
                                                                     uint16_t* __restrict__ W) {
@@ -126,12 +175,13 @@ __global__ void __launch_bounds__(kMxThreads) dequantize_mx4_kernel(const uint8_
     pdl_trigger();
     const int64_t step = (int64_t)gridDim.x * kMxThreads;
     for (int64_t c0 = (int64_t)blockIdx.x * kMxThreads + threadIdx.x; c0 < chunks; c0 += kMxUnroll * step) {
-        uint32_t q[kMxUnroll], s[kMxUnroll];
+        uint2 q[kMxUnroll];
+        uint32_t s[kMxUnroll];
 #pragma unroll
         for (int u = 0; u < kMxUnroll; ++u) {
             const int64_t c = c0 + u * step;
-            q[u] = c < chunks ? *reinterpret_cast<const uint32_t*>(Q + c * 4) : 0u;
-            s[u] = c < chunks ? S[c >> 2] : 127u;
+            q[u] = c < chunks ? __ldg(reinterpret_cast<const uint2*>(Q + c * 8)) : make_uint2(0, 0);
+            s[u] = c < chunks ? __ldg(S + (c >> 1)) : 127u;
         }
 #pragma unroll
         for (int u = 0; u < kMxUnroll; ++u) {
@@ -139,21 +189,10 @@ __global__ void __launch_bounds__(kMxThreads) dequantize_mx4_kernel(const uint8_
             if (c >= chunks) continue;
             const float sc = s[u] == 255u ? __uint_as_float(0x7FC00000u)
                                           : __uint_as_float(s[u] == 0 ? 0x00400000u : s[u] << 23);
-            uint32_t h[4], o[4];
-            asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-                "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-                "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-                "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-                "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-                "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-                : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-                : "r"(q[u]));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-                o[i] = (uint32_t)f32_to_bf16_bits(f.x * sc) | ((uint32_t)f32_to_bf16_bits(f.y * sc) << 16);
-            }
-            *reinterpret_cast<uint4*>(W + c * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+            uint32_t o[8];
+            mx_values(q[u].x, sc, o);
+            mx_values(q[u].y, sc, o + 4);
+            st_chunk<kWide>(W + c * 16, o);
         }
     }
 }
@@ -167,8 +206,9 @@ static unsigned mx_blocks(int64_t chunks, int num_sms) {
 // elements % 32 == 0.
 cudaError_t launch_quantize_mx4(const uint16_t* W, int64_t elements, uint8_t* Q, uint8_t* S, cudaStream_t st,
                                 int num_sms) {
-    return launch_pdl(quantize_mx4_kernel, dim3(mx_blocks(elements / 8, num_sms)), dim3(kMxThreads), 0, st, W,
-                      elements / 8, Q, S);
+    const auto kernel = reinterpret_cast<uintptr_t>(W) % 32 == 0 ? quantize_mx4_kernel<true> : quantize_mx4_kernel<false>;
+    return launch_pdl(kernel, dim3(mx_blocks(elements / 16, num_sms)), dim3(kMxThreads), 0, st, W,
+                      elements / 16, Q, S);
 }
 
 cudaError_t launch_quantize_mx4_rows(const uint16_t* x, const int32_t* perm, const int32_t* n_live, int64_t cap_rows,
@@ -180,8 +220,10 @@ cudaError_t launch_quantize_mx4_rows(const uint16_t* x, const int32_t* perm, con
 
 cudaError_t launch_dequantize_mx4(const uint8_t* Q, const uint8_t* S, int64_t elements, uint16_t* W, cudaStream_t st,
                                   int num_sms) {
-    return launch_pdl(dequantize_mx4_kernel, dim3(mx_blocks(elements / 8, num_sms)), dim3(kMxThreads), 0, st, Q, S,
-                      elements / 8, W);
+    const auto kernel =
+        reinterpret_cast<uintptr_t>(W) % 32 == 0 ? dequantize_mx4_kernel<true> : dequantize_mx4_kernel<false>;
+    return launch_pdl(kernel, dim3(mx_blocks(elements / 16, num_sms)), dim3(kMxThreads), 0, st, Q, S,
+                      elements / 16, W);
 }
 
 }  // namespace jmoe

@@ -63,6 +63,25 @@ def test_quantize_every_bf16_value():
     assert_quantize_equal(bits)
 
 
+@pytest.mark.parametrize("skip", [8, 24, 16])
+def test_quantize_views_off_32_bytes(skip):
+    """Rows that start on a 16-byte boundary only (or on the next 32-byte one), codes 16 and scales 4 bytes in."""
+    rng = np.random.default_rng(skip)
+    bits = synth.f32_to_bf16_bits(rng.standard_normal((5, 224)).astype(np.float32))
+    W = torch.zeros(5 * 224 + skip, dtype=torch.bfloat16, device="cuda")[skip:].view(5, 224)
+    W.copy_(bf16_to_dev(bits))
+    Q = torch.zeros(5 * 112 + 16, dtype=torch.uint8, device="cuda")
+    S = torch.zeros(5 * 7 + 8, dtype=torch.uint8, device="cuda")
+    out = Q[16:].view(5, 112), S[4:39].view(5, 7)
+    jm.jamba_moe_quantize_mx4(W, out=out)
+    q, s = ref.quantize(bits)
+    assert np.array_equal(out[0].cpu().numpy(), q) and np.array_equal(out[1].cpu().numpy(), s)
+    assert not Q[:16].any() and not S[:4].any() and not S[39:].any()
+    W.zero_()
+    jm.jamba_moe_dequantize_mx4(*out, out=W)
+    assert np.array_equal(dev_to_bf16_bits(W), ref.bf16_bits(ref.values(q, s)))
+
+
 def test_quantize_ties_at_every_scale():
     grid = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0, 7.0, 4.0])
     row = np.concatenate([grid, -grid])
