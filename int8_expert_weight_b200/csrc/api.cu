@@ -905,7 +905,7 @@ bool grouped_shape_ok(int64_t N, int64_t rows, int64_t cols, int E) {
 
 struct LayoutMx4 {
     int64_t rows_cap;
-    size_t hdr, ids, wts, inv, perm, xq, xs, h, hq, hs, slots, total;
+    size_t hdr, ids, wts, inv, perm, xq, xs, hq, hs, slots, total;
     GuardGaps guards;
 };
 
@@ -921,7 +921,6 @@ LayoutMx4 make_layout_mx4(int64_t T, int64_t d, int64_t F) {
     L.perm = R.take(sizeof(int32_t) * L.rows_cap);
     L.xq = R.take((size_t)L.rows_cap * (d / 2));
     L.xs = R.take((size_t)L.rows_cap * (d / 32));
-    L.h = R.take(sizeof(uint16_t) * L.rows_cap * F);
     L.hq = R.take((size_t)L.rows_cap * (F / 2));
     L.hs = R.take((size_t)L.rows_cap * (F / 32));
     L.slots = R.take(sizeof(float) * TK * d);
@@ -1026,7 +1025,6 @@ int jamba_moe_forward_mx4(const uint16_t* x, const float* router_W, const float*
     int32_t* perm = reinterpret_cast<int32_t*>(ws + L.perm);
     uint8_t* xq = reinterpret_cast<uint8_t*>(ws + L.xq);
     uint8_t* xs = reinterpret_cast<uint8_t*>(ws + L.xs);
-    uint16_t* h = reinterpret_cast<uint16_t*>(ws + L.h);
     uint8_t* hq = reinterpret_cast<uint8_t*>(ws + L.hq);
     uint8_t* hs = reinterpret_cast<uint8_t*>(ws + L.hs);
     float* slots = reinterpret_cast<float*>(ws + L.slots);
@@ -1069,17 +1067,13 @@ int jamba_moe_forward_mx4(const uint16_t* x, const float* router_W, const float*
     p.sa = S1;
     p.qb = Q3;
     p.sb = S3;
-    p.y16 = h;
+    p.hq = hq;
+    p.hs = hs;
     p.K = (int)d;
     p.M = (int)ffn;
     {
         TimedLaunch t(JMOE_KERNEL_GEMM13, st);
         e = launch_grouped_mx4(p, st, sms);
-    }
-    if (e != cudaSuccess) return JMOE_ERR_CUDA;
-    {
-        TimedLaunch t(JMOE_KERNEL_ACT_QUANT, st);
-        e = launch_quantize_mx4_rows(h, perm, n_rows, L.rows_cap, ffn, 0, hq, hs, st, sms);
     }
     if (e != cudaSuccess) return JMOE_ERR_CUDA;
     p.xq = hq;
@@ -1090,7 +1084,6 @@ int jamba_moe_forward_mx4(const uint16_t* x, const float* router_W, const float*
     p.sb = nullptr;
     p.perm = perm;
     p.wts = wts;
-    p.y16 = nullptr;
     p.y32 = slots;
     p.K = (int)ffn;
     p.M = (int)d;

@@ -3,7 +3,7 @@
 //
 //   plain   y[r][i]      = sum_k x^[r][k] W^_e[i][k]                   (bf16 or fp32)
 //   slot    out[a][i]    = p_a * sum_k x^[r][k] W^_e[i][k]             (fp32; a = assignment of row r)
-//   dual    h[r][j]      = bf16( SiLU(x^[r] . W1^_e[j]) * (x^[r] . W3^_e[j]) )
+//   dual    h[r][j]      = MX4( bf16( SiLU(x^[r] . W1^_e[j]) * (x^[r] . W3^_e[j]) ) )
 //
 // with v^ the value of an MX4 code times its block's scale, fp32 sums.  The tensor cores take the codes
 // and the scales as they are (tcgen05.mma kind::mxf4.block_scale): nothing is expanded.
@@ -70,7 +70,7 @@ struct Cfg {
     static constexpr int kSfWarps = 1 + kSfBlocks;          // of one set of scale warps
     static constexpr int kEpiWarp0 = 2 + 2 * kSfWarps;
     static constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
-    static constexpr int kBars = 2 * kStages + 5;
+    static constexpr int kBars = 2 * kStages + 5 + kEpiWarps / 2;
     static constexpr int kSmem = kStages * kStage + kEpiWarps * kOutBytes + 1024 + 8 * kBars;
     static_assert(kThreads >= kMaxGroups, "one thread per group");
     static_assert(kTok % 16 == 0 && kB % 1024 == 0 && kStages >= 3 && kSfSets >= 2, "tile");
@@ -116,6 +116,14 @@ __device__ __forceinline__ void tile_at(const Groups& G, const Args& p, int L, T
 // far below the bf16 rounding of h that follows.
 __device__ __forceinline__ float silu_fast(float a) { return __fdividef(a, 1.0f + __expf(-a)); }
 
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+    uint4 q;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                 : "r"(addr)
+                 : "memory");
+    return q;
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&b);
@@ -133,47 +141,47 @@ __device__ __forceinline__ void fail(WsHeader* hdr, volatile int* abort) {
 // v (see tmem_ld_16x16; lanes 0-15, then 16-31) go transposed through the warp's area `out` of shared memory and
 // leave as 16-byte pieces of y rows, element by element where rows are no multiple of 8 long.  (Trading values
 // between neighbouring lanes and storing 4 bytes each took 1200 cycles per 16 tokens.)
-// kDual: gate and up of one j are in lanes l and l + 16, so in the same place of the two halves of v.
-template <bool kDual>
 __device__ __forceinline__ void store_bf16(const Args& p, uint32_t out, const uint32_t (&v)[16], int64_t row0, int n, int j0,
                                            int lane) {
-    constexpr int kPitch = kDual ? 48 : kOutPitch, kJ = kDual ? 16 : 32;
-    if constexpr (kDual) {  // 2 j blocks x 2 token blocks of 8
-        uint32_t m[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            m[i] = pack_bf16(silu_fast(__uint_as_float(v[2 * i])) * __uint_as_float(v[8 + 2 * i]),
-                             silu_fast(__uint_as_float(v[2 * i + 1])) * __uint_as_float(v[9 + 2 * i]));
-        tc::stmatrix_x4_trans(out + (8 * (lane >> 4) + (lane & 7)) * kPitch + 16 * ((lane >> 3) & 1), m[0], m[1], m[2], m[3]);
-    } else {  // 4 j blocks, for each of two token blocks
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            tc::stmatrix_x4_trans(out + (8 * i + (lane & 7)) * kPitch + 16 * (lane >> 3), pack_bf16(v[4 * i], v[4 * i + 1]),
-                                  pack_bf16(v[4 * i + 2], v[4 * i + 3]), pack_bf16(v[8 + 4 * i], v[9 + 4 * i]),
-                                  pack_bf16(v[10 + 4 * i], v[11 + 4 * i]));
-    }
+    for (int i = 0; i < 2; ++i)  // 4 j blocks of 8, for each of two token blocks
+        tc::stmatrix_x4_trans(out + (8 * i + (lane & 7)) * kOutPitch + 16 * (lane >> 3), pack_bf16(v[4 * i], v[4 * i + 1]),
+                              pack_bf16(v[4 * i + 2], v[4 * i + 3]), pack_bf16(v[8 + 4 * i], v[9 + 4 * i]),
+                              pack_bf16(v[10 + 4 * i], v[11 + 4 * i]));
     __syncwarp();
     uint16_t* y = p.y16 + row0 * p.M + j0;
     if (p.M % 8 == 0) {
-        constexpr int kParts = kJ / 8, kToks = 32 / kParts;  // 16-byte pieces of a row; rows per store
 #pragma unroll
-        for (int i = 0; i < 16 / kToks; ++i) {
-            const int tok = kToks * i + lane / kParts, j = 8 * (lane % kParts);
-            uint4 q;
-            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
-                         : "r"(out + tok * kPitch + 2 * j)
-                         : "memory");
+        for (int i = 0; i < 2; ++i) {
+            const int tok = 8 * i + lane / 4, j = 8 * (lane % 4);
+            const uint4 q = ld_shared_v4(out + tok * kOutPitch + 2 * j);
             if (tok < n && j0 + j < p.M) *reinterpret_cast<uint4*>(y + (int64_t)tok * p.M + j) = q;
         }
     } else {
         for (int tok = 0; tok < 16 && tok < n; ++tok) {
             uint16_t q;
-            asm volatile("ld.shared.b16 %0, [%1];" : "=h"(q) : "r"(out + tok * kPitch + 2 * (lane % kJ)) : "memory");
-            if (lane < kJ && j0 + lane < p.M) y[(int64_t)tok * p.M + lane] = q;
+            asm volatile("ld.shared.b16 %0, [%1];" : "=h"(q) : "r"(out + tok * kOutPitch + 2 * lane) : "memory");
+            if (j0 + lane < p.M) y[(int64_t)tok * p.M + lane] = q;
         }
     }
     __syncwarp();  // the area is rewritten by the next 16 tokens
+}
+
+// dual: SwiGLU of 16 tokens and 16 columns j0 .. of h: gate and up of one j are in lanes l and l + 16, so in the same
+// place of the two halves of v.  As bf16 transposed through `out`; returned: 8 values of h, of token lane / 2 and
+// columns j0 + 8 (lane % 2) ...
+__device__ __forceinline__ uint4 swiglu_bf16(uint32_t out, const uint32_t (&v)[16], int lane) {
+    constexpr int kPitch = 48;
+    uint32_t m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)  // 2 j blocks x 2 token blocks of 8
+        m[i] = pack_bf16(silu_fast(__uint_as_float(v[2 * i])) * __uint_as_float(v[8 + 2 * i]),
+                         silu_fast(__uint_as_float(v[2 * i + 1])) * __uint_as_float(v[9 + 2 * i]));
+    tc::stmatrix_x4_trans(out + (8 * (lane >> 4) + (lane & 7)) * kPitch + 16 * ((lane >> 3) & 1), m[0], m[1], m[2], m[3]);
+    __syncwarp();
+    const uint4 q = ld_shared_v4(out + (lane >> 1) * kPitch + 16 * (lane & 1));
+    __syncwarp();  // the area is rewritten by the next 16 tokens
+    return q;
 }
 
 // 16 tokens (the first n of them live) of column j as fp32: y rows row0 .., or, times their routing weights, the slots of
@@ -219,6 +227,7 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ Groups G;
     __shared__ int warp_sum[C::kThreads / 32];
+    __shared__ uint32_t amax_sh[kDual ? kEpiWarps : 1][2][16];  // dual: largest |h| of 16 tokens over a warp's columns
     __shared__ uint32_t tmem_holder;
     __shared__ volatile int abort_flag;
 
@@ -269,6 +278,7 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
     uint64_t* acc_full = empty + kStages;        // [2] accumulator complete
     uint64_t* acc_empty = acc_full + 2;          // [2] accumulator read out by the epilogue
     uint64_t* mma_done = acc_empty + 2;          // every issued MMA complete (after an abort)
+    uint64_t* swap = mma_done + 1;               // [kEpiWarps / 2] dual: a pair of warps has written its magnitudes
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -280,6 +290,7 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
             tc::mbar_init(&acc_empty[b], C::kCtas * kEpiWarps);
         }
         tc::mbar_init(mma_done, 1);
+        for (int i = 0; i < kEpiWarps / 2; ++i) tc::mbar_init(&swap[i], 2);
         abort_flag = 0;
         tc::mbar_fence_init();
     }
@@ -510,24 +521,27 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
         // ---------------- epilogue, 16 tokens at a time
         const int qd = warp & 3, ew = warp - kEpiWarp0, part = ew >> 2;
         const bool bf16 = kDual || p.y16;
-        int it = 0;
+        int it = 0, swaps = 0;
         Tile t;
         for (int L = first; L < total; L += stride, ++it) {
             tile_at<kTok>(G, p, L, t);
             const int b = it & 1, u = it >> 1;
-            const bool ok = wait(&acc_full[b], u);
+            bool ok = wait(&acc_full[b], u);
             if (!__all_sync(0xffffffffu, ok)) break;  // tcgen05.ld below is warp-collective
             tc::tc_fence_after();
             const uint32_t t_lane = tmem + ((uint32_t)(32 * qd) << 16) + (uint32_t)(b * kTok);
+            const uint32_t out = tc::smem_u32(sOut + ew * kOutBytes);
             const int n_unit = (t.ntok + 15) / 16;  // this warp's: part, part + 2, ...
+            const int j0 = (t.n * C::kCtas + rank) * kRowsCta + (kDual ? 16 : 32) * qd;  // its first column of y (or h)
             auto release = [&]() {
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive(&acc_empty[b]);
             };
-            // bf16: two fragments (16 lanes x 8 tokens) of TMEM lanes 0-15 and two of lanes 16-31 of the quarter;
-            // fp32: 16 tokens of this thread's lane
-            auto load = [&](int unit, uint32_t (&v)[16]) {
+            for (int unit = part; unit < n_unit; unit += 2) {
+                // bf16: two fragments (16 lanes x 8 tokens) of TMEM lanes 0-15 and two of lanes 16-31 of the quarter;
+                // fp32: 16 tokens of this thread's lane
+                uint32_t v[16];
                 if (bf16) {
                     tc::tmem_ld_16x16(t_lane + (uint32_t)(16 * unit), v);
                     tc::tmem_ld_16x16(t_lane + (16u << 16) + (uint32_t)(16 * unit), v + 8);
@@ -535,20 +549,34 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
                     tc::tmem_ld16(t_lane + (uint32_t)(16 * unit), v);
                 }
                 tc::tmem_wait_ld();
-            };
-            const int j0 = (t.n * C::kCtas + rank) * kRowsCta + (kDual ? 16 : 32) * qd;  // this warp's first column of y
-            auto store = [&](int unit, const uint32_t (&v)[16]) {
-                if (bf16)
-                    store_bf16<kDual>(p, tc::smem_u32(sOut + ew * kOutBytes), v, t.row0 + 16 * unit, t.ntok - 16 * unit, j0, lane);
-                else
-                    store_fp32(p, v, t.row0 + 16 * unit, t.ntok - 16 * unit, j0 + lane, lane);
-            };
-            uint32_t v[16];
-            for (int unit = part; unit < n_unit; unit += 2) {
-                load(unit, v);
                 if (unit + 2 >= n_unit) release();
-                store(unit, v);
+                const int64_t row0 = t.row0 + 16 * unit;
+                const int n = t.ntok - 16 * unit;
+                if constexpr (kDual) {
+                    // h's blocks of 32 are the columns of two neighbouring warps: they trade each token's largest |h|
+                    const uint4 h = swiglu_bf16(out, v, lane);
+                    uint32_t amax = chunk_amax(h);
+                    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                    if ((lane & 1) == 0) amax_sh[ew][swaps & 1][lane >> 1] = amax;
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&swap[ew >> 1]);
+                    ok = __all_sync(0xffffffffu, wait(&swap[ew >> 1], swaps));
+                    if (!ok) break;
+                    amax = max(amax, amax_sh[ew ^ 1][swaps & 1][lane >> 1]);
+                    ++swaps;
+                    const uint32_t s = mx_scale(amax);
+                    const int tok = lane >> 1, j = j0 + 8 * (lane & 1);
+                    if (tok < n && j < p.M) {
+                        *reinterpret_cast<uint32_t*>(p.hq + (row0 + tok) * (p.M / 2) + j / 2) = mx_codes(h, s);
+                        if (j % 32 == 0) p.hs[(row0 + tok) * (p.M / 32) + j / 32] = (uint8_t)s;
+                    }
+                } else if (bf16) {
+                    store_bf16(p, out, v, row0, n, j0, lane);
+                } else {
+                    store_fp32(p, v, row0, n, j0 + lane, lane);
+                }
             }
+            if (!ok) break;
             if (part >= n_unit) release();  // a warp whose columns hold no tokens of this tile
         }
     }
