@@ -70,7 +70,7 @@ struct Cfg {
     static constexpr int kSfWarps = 1 + kSfBlocks;          // of one set of scale warps
     static constexpr int kEpiWarp0 = 2 + 2 * kSfWarps;
     static constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
-    static constexpr int kBars = 2 * kStages + 5 + kEpiWarps / 2;
+    static constexpr int kBars = 2 * kStages + 5;
     static constexpr int kSmem = kStages * kStage + kEpiWarps * kOutBytes + 1024 + 8 * kBars;
     static_assert(kThreads >= kMaxGroups, "one thread per group");
     static_assert(kTok % 16 == 0 && kB % 1024 == 0 && kStages >= 3 && kSfSets >= 2, "tile");
@@ -278,7 +278,6 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
     uint64_t* acc_full = empty + kStages;        // [2] accumulator complete
     uint64_t* acc_empty = acc_full + 2;          // [2] accumulator read out by the epilogue
     uint64_t* mma_done = acc_empty + 2;          // every issued MMA complete (after an abort)
-    uint64_t* swap = mma_done + 1;               // [kEpiWarps / 2] dual: a pair of warps has written its magnitudes
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -290,7 +289,6 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
             tc::mbar_init(&acc_empty[b], C::kCtas * kEpiWarps);
         }
         tc::mbar_init(mma_done, 1);
-        for (int i = 0; i < kEpiWarps / 2; ++i) tc::mbar_init(&swap[i], 2);
         abort_flag = 0;
         tc::mbar_fence_init();
     }
@@ -527,6 +525,7 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
             tile_at<kTok>(G, p, L, t);
             const int b = it & 1, u = it >> 1;
             bool ok = wait(&acc_full[b], u);
+            if constexpr (kDual) ok = !tc::named_sync_or(1 + (ew >> 1), 64, !ok);  // the two warps stop together or not at all
             if (!__all_sync(0xffffffffu, ok)) break;  // tcgen05.ld below is warp-collective
             tc::tc_fence_after();
             const uint32_t t_lane = tmem + ((uint32_t)(32 * qd) << 16) + (uint32_t)(b * kTok);
@@ -538,18 +537,27 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
                 __syncwarp();
                 if (lane == 0) arrive(&acc_empty[b]);
             };
-            for (int unit = part; unit < n_unit; unit += 2) {
-                // bf16: two fragments (16 lanes x 8 tokens) of TMEM lanes 0-15 and two of lanes 16-31 of the quarter;
-                // fp32: 16 tokens of this thread's lane
-                uint32_t v[16];
+            // bf16: two fragments (16 lanes x 8 tokens) of TMEM lanes 0-15 and two of lanes 16-31 of the quarter;
+            // fp32: 16 tokens of this thread's lane
+            auto load = [&](int unit, uint32_t (&v)[16]) {
                 if (bf16) {
                     tc::tmem_ld_16x16(t_lane + (uint32_t)(16 * unit), v);
                     tc::tmem_ld_16x16(t_lane + (16u << 16) + (uint32_t)(16 * unit), v + 8);
                 } else {
                     tc::tmem_ld16(t_lane + (uint32_t)(16 * unit), v);
                 }
+            };
+            uint32_t next[16];
+            if (part < n_unit) load(part, next);
+            for (int unit = part; unit < n_unit; unit += 2) {
                 tc::tmem_wait_ld();
-                if (unit + 2 >= n_unit) release();
+                uint32_t v[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = next[i];
+                if (unit + 2 < n_unit)
+                    load(unit + 2, next);
+                else
+                    release();
                 const int64_t row0 = t.row0 + 16 * unit;
                 const int n = t.ntok - 16 * unit;
                 if constexpr (kDual) {
@@ -558,10 +566,7 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
                     uint32_t amax = chunk_amax(h);
                     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                     if ((lane & 1) == 0) amax_sh[ew][swaps & 1][lane >> 1] = amax;
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&swap[ew >> 1]);
-                    ok = __all_sync(0xffffffffu, wait(&swap[ew >> 1], swaps));
-                    if (!ok) break;
+                    tc::named_sync(1 + (ew >> 1), 64);
                     amax = max(amax, amax_sh[ew ^ 1][swaps & 1][lane >> 1]);
                     ++swaps;
                     const uint32_t s = mx_scale(amax);
@@ -576,7 +581,6 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
                     store_fp32(p, v, row0, n, j0 + lane, lane);
                 }
             }
-            if (!ok) break;
             if (part >= n_unit) release();  // a warp whose columns hold no tokens of this tile
         }
     }
