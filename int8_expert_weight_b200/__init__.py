@@ -158,9 +158,15 @@ def _one_device(ref: torch.Tensor, **tensors) -> torch.device:
     return ref.device
 
 
+# The current stream's handle without a Stream object around it (2 us a call), where torch has it.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _launch(fn, dev: torch.device, stream: Optional[torch.cuda.Stream], *args) -> int:
     """fn(*args, stream) with `dev` current; the switch is left out when it is already (it costs over a microsecond)."""
     if torch.cuda.current_device() == dev.index:
+        if stream is None and _current_raw_stream is not None:
+            return fn(*args, _current_raw_stream(dev.index))
         return fn(*args, _stream_ptr(stream, dev))
     with torch.cuda.device(dev):
         return fn(*args, _stream_ptr(stream, dev))

@@ -15,12 +15,13 @@
 //   dual: rows 32q .. 32q+15 of the tile are W1 rows j0+16q .., rows 32q+16 .. 32q+31 the W3 rows of the
 //   same j (q = 0..3), so gate and up of one j sit in lanes l and l + 16 of a warp and meet with one shuffle.
 //
-// Persistent, one CTA per SM, warps in roles; a pipeline stage holds 256 of K (128 bytes of codes per row):
+// Persistent, one CTA per SM, warps in roles; a pipeline stage holds 256 of K (128 bytes of codes per row),
+// or, where each tile has few tokens, 512:
 //   warp 0      codes: TMA boxes of 128 bytes x 128 (dual: 16) weight rows and x 32 token rows, SWIZZLE_128B
-//   warp 1      TMEM allocator; per stage copies the scales to TMEM (tcgen05.cp) and issues 4 MMAs of 64 k
+//   warp 1      TMEM allocator; per stage copies the scales to TMEM (tcgen05.cp) and issues the MMAs, 64 k each
 //   4-6 warps   scales: two sets, in turns, of one warp per 128 rows of weights or tokens.  The tensor core wants 512-byte blocks of 128 rows
 //               x 128 k with row r at 16 (r % 32) + 4 (r / 32); a lane reads 32 bytes (a DRAM sector: 1024 of
-//               K, four stages) of rows lane, lane + 32, + 64, + 96 into registers, four stages ahead and across
+//               K) of rows lane, lane + 32, + 64, + 96 into registers, ahead of their use and across
 //               tiles, and stores 16 bytes per block.  (4-byte copies per row and 128 k fetched each sector
 //               eight times: 2.85 TB/s instead of 5.0 on the 64-token product.)
 //   8 warps     epilogue: two warps per TMEM lane quarter, alternate 32-column chunks
@@ -43,12 +44,12 @@ namespace jmoe {
 namespace mx4 {
 
 constexpr int kWRows = 128;
-constexpr int kStageBytes = 128;  // bytes of codes per row and stage: 256 of K
+constexpr int kSubBytes = 128;    // bytes of codes per row and sub-step: 256 of K
 constexpr int kBoxRows = 32;      // token rows per copy
 constexpr int kEpiWarps = 8;
 constexpr int kOutPitch = 80;     // bytes per token of a warp's 16-token staging area (32 bf16, plus 16: no bank conflicts)
 constexpr int kOutBytes = 16 * kOutPitch;
-constexpr int kSfStages = 4;      // stages whose scales a lane holds: 32 bytes of each of its rows
+constexpr int kSfWords = 8;       // words of scales that a lane holds of each of its rows: 32 bytes
 constexpr uint32_t kMaxPolls = 1u << 22;  // ~0.3 s of polling: far above any healthy wait
 
 // kPair: two CTAs work on one tile of 256 weight rows.
@@ -56,17 +57,23 @@ template <bool kPair, int kTok>
 struct Cfg {
     static constexpr int kCtas = kPair ? 2 : 1;
     static constexpr int kTokCta = kTok / kCtas;            // token rows whose codes a CTA holds
-    static constexpr int kSfBlocks = (kTok + 127) / 128;    // 512-byte blocks of token scales per 128 k
-    static constexpr int kA = kWRows * kStageBytes;
-    static constexpr int kB = kTokCta * kStageBytes;
-    static constexpr int kSfA = 2 * 512;
-    static constexpr int kSfB = 2 * kSfBlocks * 512;
+    // Sub-steps of 256 k in a stage.  With few tokens a sub-step's MMAs are short and the hand-over of a stage costs as
+    // much, so two share one (two rows x 4096 x 14336: 17.5 or 17.0 us; the layer on one token: 67.5 or 63.6 us).
+    static constexpr int kSub = kPair ? 1 : 2;
+    static constexpr int kWords = 2 * kSub;                 // of 128 k: the scales' unit
+    static constexpr int kSfBlocks = (kTok + 127) / 128;    // 512-byte blocks of token scales per word
+    static constexpr int kASub = kWRows * kSubBytes, kBSub = kTokCta * kSubBytes;
+    static constexpr int kA = kSub * kASub;
+    static constexpr int kB = kSub * kBSub;
+    static constexpr int kSfA = kWords * 512;
+    static constexpr int kSfB = kWords * kSfBlocks * 512;
     static constexpr int kStage = kA + kB + kSfA + kSfB;
     static constexpr int kStages = (227 * 1024 - 6 * 1024 - kEpiWarps * kOutBytes) / kStage;
-    static constexpr int kSfCols = 8 + 8 * kSfBlocks;
+    static constexpr int kSfCols = kWords * 4 * (1 + kSfBlocks);
     static constexpr int kSfCol0 = 2 * kTok;
     static constexpr int kSfSets = (512 - kSfCol0) / kSfCols < kStages ? (512 - kSfCol0) / kSfCols : kStages;
     static constexpr uint32_t kTmemCols = kSfCol0 + kSfSets * kSfCols <= 256 ? 256 : 512;
+    static constexpr int kSfStages = kSfWords / kWords;     // stages whose scales a lane holds
     static constexpr int kSfWarps = 1 + kSfBlocks;          // of one set of scale warps
     static constexpr int kEpiWarp0 = 2 + 2 * kSfWarps;
     static constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
@@ -205,14 +212,14 @@ __device__ __forceinline__ void store_fp32(const Args& p, const uint32_t (&v)[16
 }
 
 // 32 bytes of scales; `vec`: 32-byte aligned and whole, else `words` 4-byte words of them are there.
-__device__ __forceinline__ void ld_scales(const uint8_t* ptr, bool vec, int words, uint32_t (&v)[2 * kSfStages]) {
+__device__ __forceinline__ void ld_scales(const uint8_t* ptr, bool vec, int words, uint32_t (&v)[kSfWords]) {
     if (vec) {
         asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
                      : "l"(ptr));
     } else {
 #pragma unroll
-        for (int i = 0; i < 2 * kSfStages; ++i)
+        for (int i = 0; i < kSfWords; ++i)
             v[i] = i < words ? __ldg(reinterpret_cast<const uint32_t*>(ptr) + i) : 0u;
     }
 }
@@ -222,7 +229,7 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
     gemm_mx4_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXs,
                     const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUtensorMap tmW1, Args p) {
     using C = Cfg<kPair, kTok>;
-    constexpr int kStages = C::kStages, kEpiWarp0 = C::kEpiWarp0;
+    constexpr int kStages = C::kStages, kSfStages = C::kSfStages, kWords = C::kWords, kEpiWarp0 = C::kEpiWarp0;
     constexpr int kRowsCta = kDual ? kWRows / 2 : kWRows;  // weight rows (of each matrix) of a CTA's part of a tile
     extern __shared__ uint8_t smem_raw[];
     __shared__ Groups G;
@@ -310,7 +317,7 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
     tc::tc_fence_after();
     const uint32_t tmem = tmem_holder;
     const int KW = p.K / 128;          // 4-byte words of scales per row
-    const int KB = (KW + 1) / 2;       // stages per tile; the last may hold one word only
+    const int KB = (KW + kWords - 1) / kWords;  // stages per tile; the last need not be whole
     int issued = 0;                    // codes: stages copied; MMA issuer: stages multiplied
     auto wait = [&](uint64_t* bar, int round) -> bool {
         if (tc::mbar_wait_bounded(bar, round & 1, &abort_flag, kMaxPolls)) return true;
@@ -339,33 +346,35 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
             const int x_row0 = (int)t.row0 + rank * part;
             // one copy for a tile (nearly) full of tokens, else the 32-row boxes it needs
             const int n_box = part > C::kTokCta / kBoxRows * kBoxRows ? 0 : (part + kBoxRows - 1) / kBoxRows;
-            const uint32_t bytes = C::kCtas * (C::kA + (n_box == 0 ? C::kTokCta : n_box * kBoxRows) * kStageBytes);
+            const uint32_t sub_bytes = C::kCtas * (C::kASub + (n_box == 0 ? C::kTokCta : n_box * kBoxRows) * kSubBytes);
             for (int kb = 0; kb < KB; ++kb, ++g) {
                 const int s = g % kStages, r = g / kStages;
                 if (r > 0 && !(ok = wait(&empty[s], r - 1))) break;
-                uint8_t* da = sA + s * C::kA;
-                uint8_t* db = sB + s * C::kB;
-                const int x = kb * kStageBytes;
+                const int n_sub = min(C::kSub, (KW - kb * kWords + 1) / 2);
                 if (tc::elect_one()) {
-                    if (rank == 0) tc::mbar_arrive_expect_tx(&full[s], bytes);
-                    auto load = [&](uint8_t* dst, const CUtensorMap* tm, int row) {
-                        if constexpr (kPair)
-                            tc::tma_load_2d_pair(dst, tm, tc::map_to_cta(tc::smem_u32(&full[s]), 0), x, row);
-                        else
-                            tc::tma_load_2d(dst, tm, &full[s], x, row);
-                    };
-                    if (kDual) {
+                    if (rank == 0) tc::mbar_arrive_expect_tx(&full[s], n_sub * sub_bytes);
+                    for (int sub = 0; sub < n_sub; ++sub) {
+                        const int x = (kb * C::kSub + sub) * kSubBytes;
+                        auto load = [&](uint8_t* dst, const CUtensorMap* tm, int row) {
+                            if constexpr (kPair)
+                                tc::tma_load_2d_pair(dst, tm, tc::map_to_cta(tc::smem_u32(&full[s]), 0), x, row);
+                            else
+                                tc::tma_load_2d(dst, tm, &full[s], x, row);
+                        };
+                        uint8_t* da = sA + s * C::kA + sub * C::kASub;
+                        uint8_t* db = sB + s * C::kB + sub * C::kBSub;
+                        if (kDual) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            load(da + q * 32 * kStageBytes, &tmW0, w_row0 + 16 * q);
-                            load(da + (q * 32 + 16) * kStageBytes, &tmW1, w_row0 + 16 * q);
+                            for (int q = 0; q < 4; ++q) {
+                                load(da + q * 32 * kSubBytes, &tmW0, w_row0 + 16 * q);
+                                load(da + (q * 32 + 16) * kSubBytes, &tmW1, w_row0 + 16 * q);
+                            }
+                        } else {
+                            load(da, &tmW0, w_row0);
                         }
-                    } else {
-                        load(da, &tmW0, w_row0);
+                        if (n_box == 0) load(db, &tmX, x_row0);
+                        for (int i = 0; i < n_box; ++i) load(db + i * kBoxRows * kSubBytes, &tmXs, x_row0 + i * kBoxRows);
                     }
-                    if (n_box == 0) load(db, &tmX, x_row0);
-                    for (int i = 0; i < n_box; ++i)
-                        load(db + i * kBoxRows * kStageBytes, &tmXs, x_row0 + i * kBoxRows);
                 }
                 __syncwarp();
                 issued = g + 1;
@@ -413,19 +422,19 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
             }
         };
         // Loads this set's next stages; returns how many (0: past the last tile), `at`: the first one.
-        auto fetch = [&](uint32_t (&v)[4][2 * kSfStages], int& at) -> int {
+        auto fetch = [&](uint32_t (&v)[4][kSfWords], int& at) -> int {
             if (L >= total) return 0;
             if (opened != L) open_tile();
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (i < live) ld_scales(ptr[i] + 8 * kb, p.vec_scales, KW - 2 * kb, v[i]);
+                if (i < live) ld_scales(ptr[i] + 4 * kWords * kb, p.vec_scales, KW - kWords * kb, v[i]);
             at = g_load;
             const int n = min(kSfStages, KB - kb);
             skip();
             if (L < total) skip();
             return n;
         };
-        uint32_t cur[4][2 * kSfStages] = {}, nxt[4][2 * kSfStages] = {};
+        uint32_t cur[4][kSfWords] = {}, nxt[4][kSfWords] = {};
         if (set == 1) skip();
         int g = 0, g_next = 0;
         bool ok = true;
@@ -438,10 +447,10 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
                 const bool free_ = r == 0 || wait(&empty[s], r - 1);
                 if (!(ok = __all_sync(0xffffffffu, free_))) break;
 #pragma unroll
-                for (int w = 0; w < 2; ++w)
+                for (int w = 0; w < kWords; ++w)
                     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst0 + s * dst_stage + w * dst_word),
-                                 "r"(cur[0][2 * st + w]), "r"(cur[1][2 * st + w]), "r"(cur[2][2 * st + w]),
-                                 "r"(cur[3][2 * st + w])
+                                 "r"(cur[0][kWords * st + w]), "r"(cur[1][kWords * st + w]), "r"(cur[2][kWords * st + w]),
+                                 "r"(cur[3][kWords * st + w])
                                  : "memory");
                 tc::fence_proxy_async_smem();
                 __syncwarp();
@@ -450,7 +459,7 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 2 * kSfStages; ++j) cur[i][j] = nxt[i][j];
+                for (int j = 0; j < kSfWords; ++j) cur[i][j] = nxt[i][j];
             n = n_next;
             g = g_next;
         }
@@ -472,9 +481,9 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
             const int n_mma = (t.ntok + 15) & ~15;
             const uint32_t idesc0 = tc::idesc_mx4_f32(C::kCtas * kWRows, n_mma, 0);
             const uint32_t idesc2 = tc::idesc_mx4_f32(C::kCtas * kWRows, n_mma, 2);
-            const int b = it & 1, u = it >> 1;
-            if (u > 0 && !(ok = wait(&acc_empty[b], u - 1))) break;
-            const uint32_t d_tmem = tmem + (uint32_t)(b * kTok);
+            const int buf = it & 1, u = it >> 1;
+            if (u > 0 && !(ok = wait(&acc_empty[buf], u - 1))) break;
+            const uint32_t d_tmem = tmem + (uint32_t)(buf * kTok);
             for (int kb = 0; kb < KB; ++kb, ++g) {
                 const int s = g % kStages, r = g / kStages;
                 if (!(ok = wait(&full[s], r))) break;
@@ -488,25 +497,29 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
                     const uint64_t adesc = adesc0 + (uint32_t)(s * (C::kA >> 4)), bdesc = bdesc0 + (uint32_t)(s * (C::kB >> 4));
                     const uint64_t sadesc = sadesc0 + (uint32_t)(s * (C::kSfA >> 4));
                     const uint64_t sbdesc = sbdesc0 + (uint32_t)(s * (C::kSfB >> 4));
-                    // 512 bytes = +32 in a descriptor's address field; the second 128 k of a last stage need not be there
+                    // 512 bytes = +32 in a descriptor's address field; a last stage need not hold all words
+                    const int words = min(kWords, KW - kb * kWords);
 #pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        tc::tmem_cp_32x16<kPair>(sf + 4 * w, sadesc + 32 * w);
+                    for (int w = 0; w < kWords; ++w) {
+                        const uint32_t sfa = sf + 4 * w, sfb = sf + 4 * kWords + 4 * C::kSfBlocks * w;
+                        tc::tmem_cp_32x16<kPair>(sfa, sadesc + 32 * w);
 #pragma unroll
                         for (int i = 0; i < C::kSfBlocks; ++i)
-                            tc::tmem_cp_32x16<kPair>(sf + 8 + 4 * (C::kSfBlocks * w + i), sbdesc + 32 * (C::kSfBlocks * w + i));
+                            tc::tmem_cp_32x16<kPair>(sfb + 4 * i, sbdesc + 32 * (C::kSfBlocks * w + i));
                     }
                     // 64 k = 32 bytes of the 128-byte row = +2 in the address field
 #pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        if (w == 0 || 2 * kb + 1 < KW) {
-                            const uint32_t sfa = sf + 4 * w, sfb = sf + 8 + 4 * C::kSfBlocks * w;
-                            tc::mma_mx4_ss<kPair>(d_tmem, adesc + 4 * w, bdesc + 4 * w, idesc0, sfa, sfb, (kb | w) != 0);
-                            tc::mma_mx4_ss<kPair>(d_tmem, adesc + 4 * w + 2, bdesc + 4 * w + 2, idesc2, sfa, sfb, 1);
+                    for (int w = 0; w < kWords; ++w) {
+                        if (w < words) {
+                            const uint32_t sfa = sf + 4 * w, sfb = sf + 4 * kWords + 4 * C::kSfBlocks * w;
+                            const uint64_t a = adesc + (w >> 1) * (C::kASub >> 4) + 4 * (w & 1);
+                            const uint64_t b = bdesc + (w >> 1) * (C::kBSub >> 4) + 4 * (w & 1);
+                            tc::mma_mx4_ss<kPair>(d_tmem, a, b, idesc0, sfa, sfb, (kb | w) != 0);
+                            tc::mma_mx4_ss<kPair>(d_tmem, a + 2, b + 2, idesc2, sfa, sfb, 1);
                         }
                     }
                     commit(&empty[s]);
-                    if (kb == KB - 1) commit(&acc_full[b]);
+                    if (kb == KB - 1) commit(&acc_full[buf]);
                 }
                 __syncwarp();
                 issued = g + 1;
@@ -637,7 +650,7 @@ bool make_map(CUtensorMap* m, const uint8_t* ptr, uint64_t rows, uint64_t row_by
     if (!fn) return false;
     cuuint64_t dims[2] = {row_bytes, rows};
     cuuint64_t strides[1] = {row_bytes};
-    cuuint32_t box[2] = {kStageBytes, box_rows};
+    cuuint32_t box[2] = {kSubBytes, box_rows};
     cuuint32_t estr[2] = {1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(ptr), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -698,7 +711,9 @@ cudaError_t launch(Args p, cudaStream_t st, int num_sms) {
 
 cudaError_t launch_grouped_mx4(const mx4::Args& p, cudaStream_t st, int num_sms) {
     using namespace mx4;
-    // few rows per expert: single CTAs with narrow token tiles, whose stages are the weights in flight
+    // Few rows per expert: single CTAs with narrow token tiles, whose stages are the weights in flight; else pairs.  Single
+    // or pairs, us, 14336 x 4096 weights of 16 experts, by rows of each: 4: 79 / 84, 48: 85 / 89, 64: 86 / 90, 96: 104 / 94,
+    // 128: 120 / 97.  A group over 64 rows takes two narrow tiles, and uneven groups reach that at a mean of 48.
     const bool few = p.rows <= (int64_t)48 * p.E;
     if (p.qb) return few ? launch<true, false, 64>(p, st, num_sms) : launch<true, true, 208>(p, st, num_sms);
     return few ? launch<false, false, 64>(p, st, num_sms) : launch<false, true, 208>(p, st, num_sms);
