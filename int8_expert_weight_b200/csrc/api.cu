@@ -978,6 +978,7 @@ int jamba_moe_grouped_mx4(const uint8_t* xq, const uint8_t* xs, const int32_t* o
     p.begin = offsets;
     p.E = n_experts;
     p.reset_status = 1;
+    p.skip_copy = 1;
     p.N = N;
     p.rows = N;
     p.xq = xq;
@@ -1067,6 +1068,7 @@ int jamba_moe_forward_mx4(const uint16_t* x, const float* router_W, const float*
     p.sa = S1;
     p.qb = Q3;
     p.sb = S3;
+    p.skip_copy = 1;
     p.hq = hq;
     p.hs = hs;
     p.K = (int)d;
@@ -1082,6 +1084,7 @@ int jamba_moe_forward_mx4(const uint16_t* x, const float* router_W, const float*
     p.sa = S2;
     p.qb = nullptr;
     p.sb = nullptr;
+    p.skip_copy = 0;
     p.perm = perm;
     p.wts = wts;
     p.y32 = slots;

@@ -41,6 +41,9 @@
 #include "tc.cuh"
 
 namespace jmoe {
+namespace ts {
+extern int g_skip_copy;  // set by jamba_moe_debug_skip_copy (tests only)
+}
 namespace mx4 {
 
 constexpr int kWRows = 128;
@@ -50,7 +53,8 @@ constexpr int kEpiWarps = 8;
 constexpr int kOutPitch = 80;     // bytes per token of a warp's 16-token staging area (32 bf16, plus 16: no bank conflicts)
 constexpr int kOutBytes = 16 * kOutPitch;
 constexpr int kSfWords = 8;       // words of scales that a lane holds of each of its rows: 32 bytes
-constexpr uint32_t kMaxPolls = 1u << 22;  // ~0.3 s of polling: far above any healthy wait
+constexpr uint32_t kMaxPolls = 1u << 22;      // ~0.3 s of polling: far above any healthy wait
+constexpr uint32_t kTestMaxPolls = 1u << 14;  // short bound used together with the test hook
 
 // kPair: two CTAs work on one tile of 256 weight rows.
 template <bool kPair, int kTok>
@@ -320,7 +324,7 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
     const int KB = (KW + kWords - 1) / kWords;  // stages per tile; the last need not be whole
     int issued = 0;                    // codes: stages copied; MMA issuer: stages multiplied
     auto wait = [&](uint64_t* bar, int round) -> bool {
-        if (tc::mbar_wait_bounded(bar, round & 1, &abort_flag, kMaxPolls)) return true;
+        if (tc::mbar_wait_bounded(bar, round & 1, &abort_flag, p.max_polls)) return true;
         if (!abort_flag) fail(p.hdr, &abort_flag);
         return false;
     };
@@ -350,6 +354,7 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
             for (int kb = 0; kb < KB; ++kb, ++g) {
                 const int s = g % kStages, r = g / kStages;
                 if (r > 0 && !(ok = wait(&empty[s], r - 1))) break;
+                if (p.skip_copy && blockIdx.x == 0 && g == 1) continue;
                 const int n_sub = min(C::kSub, (KW - kb * kWords + 1) / 2);
                 if (tc::elect_one()) {
                     if (rank == 0) tc::mbar_arrive_expect_tx(&full[s], n_sub * sub_bytes);
@@ -607,11 +612,11 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
                 if (s >= issued) continue;
                 const int last = (issued - 1 - s) / kStages;
                 // a copy of round r completes phase `last` of full[s] once the scales are there too, else this wait runs out
-                for (uint32_t i = 0; i < kMaxPolls && !tc::mbar_try_wait(&full[s], last & 1); ++i) __nanosleep(64);
+                for (uint32_t i = 0; i < p.max_polls && !tc::mbar_try_wait(&full[s], last & 1); ++i) __nanosleep(64);
             }
         }
         if (warp == 1 && lane == 0) {  // completes if the issuer gave up; if it did not, its last MMAs are long done after this
-            for (uint32_t i = 0; i < kMaxPolls && !tc::mbar_try_wait(mma_done, 0); ++i) __nanosleep(64);
+            for (uint32_t i = 0; i < p.max_polls && !tc::mbar_try_wait(mma_done, 0); ++i) __nanosleep(64);
         }
         __syncthreads();
     }
@@ -684,6 +689,8 @@ cudaError_t launch(Args p, cudaStream_t st, int num_sms) {
     const uintptr_t scales = reinterpret_cast<uintptr_t>(p.xs) | reinterpret_cast<uintptr_t>(p.sa) |
                              reinterpret_cast<uintptr_t>(kDual ? p.sb : p.sa);
     p.vec_scales = p.K % 1024 == 0 && scales % 32 == 0;
+    p.max_polls = ts::g_skip_copy ? kTestMaxPolls : kMaxPolls;
+    if (!ts::g_skip_copy) p.skip_copy = 0;
     // token tiles per band: the band's codes near 32 MB of L2
     const int64_t per_tile = (int64_t)kTok * (p.K / 2);
     p.band_max = (int)(per_tile >= (32ll << 20) ? 1 : (32ll << 20) / per_tile);

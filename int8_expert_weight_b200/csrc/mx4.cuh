@@ -69,6 +69,8 @@ struct Args {
     int K;                 // reduction length
     int M;                 // weight rows per expert and matrix
     int n_wt;              // weight tiles per expert (set by the launcher)
+    int skip_copy;         // test hook, heeded while it is on: CTA 0 skips the copies of its second stage
+    uint32_t max_polls;    // bound of every mbarrier wait (set by the launcher)
     int vec_scales;        // rows of scales are whole 32-byte pieces on 32-byte boundaries (set by the launcher)
     int band_max;          // token tiles per L2 band, at most (set by the launcher)
 };

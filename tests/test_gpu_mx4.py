@@ -257,6 +257,25 @@ def test_grouped_graph_and_streams():
         assert np.array_equal(got[k].cpu().numpy(), want[k])
 
 
+@pytest.mark.parametrize("counts", [[3, 40, 8], [300, 5, 209]])  # single CTAs, pairs
+def test_grouped_wait_runs_out(counts):
+    """A copy left out: the wait for it runs out, the call reports it and returns; the next call is right."""
+    rng = np.random.default_rng(15)
+    n = sum(counts)
+    x, w = operands(rng, n, 300, 4096, 3, [127])
+    ws = torch.empty(jm.jamba_moe_grouped_mx4_workspace_size(n, 300, 4096, 3), dtype=torch.uint8, device="cuda")
+    args = [cuda(x[0]), cuda(x[1]), cuda(offsets_of(counts).astype(np.int32)), cuda(w[0]), cuda(w[1])]
+    jm.jamba_moe_debug_skip_copy(True)
+    try:
+        jm.jamba_moe_grouped_mx4(*args, out_dtype=torch.float32, workspace=ws)
+        assert jm.jamba_moe_read_device_status(ws) == 5
+    finally:
+        jm.jamba_moe_debug_skip_copy(False)
+    y = jm.jamba_moe_grouped_mx4(*args, out_dtype=torch.float32, workspace=ws)
+    assert jm.jamba_moe_read_device_status(ws) == 0
+    assert np.array_equal(y.cpu().numpy(), ref.grouped(ref.values(*x), offsets_of(counts), ref.values(*w))[0])
+
+
 def test_grouped_deterministic():
     rng = np.random.default_rng(14)
     x, w = operands(rng, 700, 300, 4096, 4, range(110, 140))
@@ -325,6 +344,21 @@ def test_layer_one_expert_and_checks():
     assert (ids.cpu().numpy() == [3, 11]).all()
     assert_y_close(dev_to_bf16_bits(y), L.ref()[0])
     assert torch.equal(y, L.forward()[0])  # the same bits again, with a new workspace
+
+
+@pytest.mark.parametrize("T", [20, 900])  # single CTAs, pairs
+def test_layer_wait_runs_out(T):
+    L = Layer(T, 1024, 256)
+    ws = torch.empty(jm.jamba_moe_workspace_size_mx4(T, 1024, 256), dtype=torch.uint8, device="cuda")
+    want = L.forward()[0]
+    jm.jamba_moe_debug_skip_copy(True)
+    try:
+        L.forward(workspace=ws)
+        assert jm.jamba_moe_read_device_status(ws) == 5
+    finally:
+        jm.jamba_moe_debug_skip_copy(False)
+    assert torch.equal(L.forward(workspace=ws)[0], want)
+    assert jm.jamba_moe_read_device_status(ws) == 0
 
 
 def test_layer_no_tokens():
