@@ -64,8 +64,9 @@ cudaError_t launch_gemm2_f8(WsHeader* hdr, const int32_t* perm, const uint8_t* h
 
 cudaError_t launch_quantize_mx4(const uint16_t* W, int64_t elements, uint8_t* Q, uint8_t* S, cudaStream_t st,
                                 int num_sms);
-cudaError_t launch_quantize_mx4_rows(const uint16_t* x, const int32_t* perm, const int32_t* n_live, int64_t cap_rows,
-                                     int64_t cols, int k_div, uint8_t* Q, uint8_t* S, cudaStream_t st, int num_sms);
+cudaError_t launch_quantize_mx4_tokens(const uint16_t* x, const int32_t* inv, const int32_t* perm, int64_t T,
+                                       int64_t cap_rows, int64_t cols, uint8_t* Q, uint8_t* S, cudaStream_t st,
+                                       int num_sms);
 cudaError_t launch_dequantize_mx4(const uint8_t* Q, const uint8_t* S, int64_t elements, uint16_t* W, cudaStream_t st,
                                   int num_sms);
 cudaError_t launch_grouped_mx4(const mx4::Args& p, cudaStream_t st, int num_sms);
@@ -1049,10 +1050,9 @@ int jamba_moe_forward_mx4(const uint16_t* x, const float* router_W, const float*
     if (e != cudaSuccess) return JMOE_ERR_CUDA;
     if (debug_step(kAfterPermute, ws, L.guards, hdr, ids, perm, inv, TK, L.rows_cap, st) != cudaSuccess)
         return JMOE_ERR_CUDA;
-    const int32_t* n_rows = &hdr->seg_start[kExperts];
     {
-        TimedLaunch t(JMOE_KERNEL_ACT_QUANT, st);  // x rows in permuted order
-        e = launch_quantize_mx4_rows(x, perm, n_rows, L.rows_cap, d, kTopK, xq, xs, st, sms);
+        TimedLaunch t(JMOE_KERNEL_ACT_QUANT, st);  // x, in permuted order
+        e = launch_quantize_mx4_tokens(x, inv, perm, T, L.rows_cap, d, xq, xs, st, sms);
     }
     if (e != cudaSuccess) return JMOE_ERR_CUDA;
     mx4::Args p{};

@@ -51,12 +51,6 @@ __device__ __forceinline__ void st_chunk(uint16_t* p, const uint32_t (&o)[8]) {
     }
 }
 
-// The block's largest magnitude across the four lanes that hold it.
-__device__ __forceinline__ uint32_t block_amax(uint32_t a) {
-    a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
-    return max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-}
-
 template <bool kWide>
 __global__ void __launch_bounds__(kMxThreads) quantize_mx4_kernel(const uint16_t* __restrict__ W, int64_t chunks,
                                                                   uint8_t* __restrict__ Q, uint8_t* __restrict__ S) {
@@ -83,29 +77,37 @@ __global__ void __launch_bounds__(kMxThreads) quantize_mx4_kernel(const uint16_t
     }
 }
 
-// The layer's x in permuted order: row r takes x row perm[r] / k_div; rows whose entry is -1 (padding) and rows from
-// *n_live on are skipped.  One CTA per row.
+// The layer's x in permuted order: the codes and scales of token t go to the rows inv[t * K + k] of its K assignments,
+// so a token is read and rounded once.  An assignment that the permutation skipped (a routing id out of range: its
+// row does not name it) is left out.  One CTA per token.
+template <bool kWide>
 __global__ void __launch_bounds__(kMxThreads)
-    quantize_mx4_rows_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ perm,
-                             const int32_t* __restrict__ n_live, int64_t cap_rows, int cols, int k_div,
-                             uint8_t* __restrict__ Q, uint8_t* __restrict__ S) {
+    quantize_mx4_tokens_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ inv,
+                               const int32_t* __restrict__ perm, int64_t T, int64_t cap_rows, int cols,
+                               uint8_t* __restrict__ Q, uint8_t* __restrict__ S) {
     pdl_wait();
     pdl_trigger();
-    const int64_t rows = min((int64_t)*n_live, cap_rows);
-    const int chunks = cols / 8;
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-        const int32_t a = perm[r];
-        if (a < 0) continue;
-        const uint16_t* xr = x + (int64_t)(a / k_div) * cols;
-        uint8_t* qr = Q + r * (cols / 2);
-        uint8_t* sr = S + r * (cols / 32);
-        for (int c0 = 0; c0 < chunks; c0 += kMxThreads) {
+    const int chunks = cols / 16;
+    for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+        int64_t rows[kTopK];
+#pragma unroll
+        for (int k = 0; k < kTopK; ++k) {
+            const int32_t r = inv[t * kTopK + k];
+            rows[k] = r >= 0 && r < cap_rows && perm[r] == t * kTopK + k ? r : -1;
+        }
+        for (int c0 = 0; c0 < chunks; c0 += blockDim.x) {  // chunks is even and a block is two lanes of one warp
             const int c = c0 + threadIdx.x;
-            const uint4 v = c < chunks ? ld_nc_v4(xr + (int64_t)c * 8) : make_uint4(0, 0, 0, 0);
-            const uint32_t s = mx_scale(block_amax(chunk_amax(v)));
+            const Chunk v = c < chunks ? ld_chunk<kWide>(x + t * cols + (int64_t)c * 16) : Chunk{};
+            const uint32_t m = max(chunk_amax(v.a), chunk_amax(v.b));
+            const uint32_t s = mx_scale(max(m, __shfl_xor_sync(0xffffffffu, m, 1)));
             if (c >= chunks) continue;
-            *reinterpret_cast<uint32_t*>(qr + c * 4) = mx_codes(v, s);
-            if ((c & 3) == 0) sr[c >> 2] = (uint8_t)s;
+            const uint2 q = make_uint2(mx_codes(v.a, s), mx_codes(v.b, s));
+#pragma unroll
+            for (int k = 0; k < kTopK; ++k) {
+                if (rows[k] < 0) continue;
+                *reinterpret_cast<uint2*>(Q + rows[k] * (cols / 2) + c * 8) = q;
+                if ((c & 1) == 0) S[rows[k] * (cols / 32) + (c >> 1)] = (uint8_t)s;
+            }
         }
     }
 }
@@ -177,11 +179,15 @@ cudaError_t launch_quantize_mx4(const uint16_t* W, int64_t elements, uint8_t* Q,
                       elements / 16, Q, S);
 }
 
-cudaError_t launch_quantize_mx4_rows(const uint16_t* x, const int32_t* perm, const int32_t* n_live, int64_t cap_rows,
-                                     int64_t cols, int k_div, uint8_t* Q, uint8_t* S, cudaStream_t st, int num_sms) {
-    const int64_t cap = (int64_t)num_sms * 8;
-    return launch_pdl(quantize_mx4_rows_kernel, dim3((unsigned)(cap_rows > cap ? cap : cap_rows)), dim3(kMxThreads), 0,
-                      st, x, perm, n_live, cap_rows, (int)cols, k_div, Q, S);
+cudaError_t launch_quantize_mx4_tokens(const uint16_t* x, const int32_t* inv, const int32_t* perm, int64_t T,
+                                       int64_t cap_rows, int64_t cols, uint8_t* Q, uint8_t* S, cudaStream_t st,
+                                       int num_sms) {
+    const int64_t cap = (int64_t)num_sms * 16;
+    const int threads = cols / 16 >= kMxThreads ? kMxThreads : (int)(cols / 16 + 31) / 32 * 32;
+    const auto kernel =
+        reinterpret_cast<uintptr_t>(x) % 32 == 0 ? quantize_mx4_tokens_kernel<true> : quantize_mx4_tokens_kernel<false>;
+    return launch_pdl(kernel, dim3((unsigned)(T > cap ? cap : T)), dim3(threads), 0, st, x, inv, perm, T, cap_rows,
+                      (int)cols, Q, S);
 }
 
 cudaError_t launch_dequantize_mx4(const uint8_t* Q, const uint8_t* S, int64_t elements, uint16_t* W, cudaStream_t st,

@@ -346,6 +346,23 @@ def test_layer_one_expert_and_checks():
     assert torch.equal(y, L.forward()[0])  # the same bits again, with a new workspace
 
 
+def test_layer_bad_routing_id_is_reported():
+    """The corruption hook puts one routing id out of range: reported, the other tokens' results are right."""
+    L = Layer(70, 256, 256)
+    ws = torch.empty(jm.jamba_moe_workspace_size_mx4(70, 256, 256), dtype=torch.uint8, device="cuda")
+    want = L.forward()[0]
+    ws.fill_(0x11)
+    jm.jamba_moe_debug_corrupt(jm.CORRUPT_ROUTE_ID)  # of assignment 0: token 0
+    y = L.forward(workspace=ws)[0]
+    assert jm.jamba_moe_read_device_status(ws) == 6
+    assert torch.equal(y[1:], want[1:])
+    # x on a 16-byte boundary only
+    x = torch.zeros(70 * 256 + 8, dtype=torch.bfloat16, device="cuda")[8:].view(70, 256)
+    x.copy_(bf16_to_dev(L.x))
+    y = jm.jamba_moe_forward_mx4(x, torch.from_numpy(L.wr).cuda(), None if L.bias is None else cuda(L.bias), *L.dev)[0]
+    assert torch.equal(y, want)
+
+
 @pytest.mark.parametrize("T", [20, 900])  # single CTAs, pairs
 def test_layer_wait_runs_out(T):
     L = Layer(T, 1024, 256)
