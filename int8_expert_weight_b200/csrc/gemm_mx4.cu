@@ -13,26 +13,39 @@
 // only have to fill up a multiple of 16.  The rows of a group start anywhere: a copy of the tile reads past the
 // group's end into the next one's rows, whose columns of the result are not stored.
 //   dual: rows 32q .. 32q+15 of the tile are W1 rows j0+16q .., rows 32q+16 .. 32q+31 the W3 rows of the
-//   same j (q = 0..3), so gate and up of one j sit in lanes l and l + 16 of a warp and meet with one shuffle.
+//   same j (q = 0..3), so gate and up of one j sit in lanes l and l + 16 of a warp: the same place of two fragments.
 //
-// Persistent, one CTA per SM, warps in roles; a pipeline stage holds 256 of K (128 bytes of codes per row),
+// Many rows per expert: a pair of CTAs (cta_group::2) works on 256 weight rows x up to 208 rows of x; each
+// holds the codes of its 128 weight rows and of half the rows of x, 29 instead of 43 KB per 256 of K, which is what
+// bounds single CTAs (16384 x 14336 x 4096: 627 us single, 573 us in pairs, all else equal).  Few rows: single CTAs,
+// tiles of 64 rows of x, the stages full of weights in flight.
+//
+// Persistent, one CTA per SM, warps in roles; a pipeline stage holds 256 of K (128 bytes of codes per row)
 // or, where each tile has few tokens, 512:
-//   warp 0      codes: TMA boxes of 128 bytes x 128 (dual: 16) weight rows and x 32 token rows, SWIZZLE_128B
-//   warp 1      TMEM allocator; per stage copies the scales to TMEM (tcgen05.cp) and issues the MMAs, 64 k each
-//   4-6 warps   scales: two sets, in turns, of one warp per 128 rows of weights or tokens.  The tensor core wants 512-byte blocks of 128 rows
-//               x 128 k with row r at 16 (r % 32) + 4 (r / 32); a lane reads 32 bytes (a DRAM sector: 1024 of
-//               K) of rows lane, lane + 32, + 64, + 96 into registers, ahead of their use and across
-//               tiles, and stores 16 bytes per block.  (4-byte copies per row and 128 k fetched each sector
-//               eight times: 2.85 TB/s instead of 5.0 on the 64-token product.)
-//   8 warps     epilogue: two warps per TMEM lane quarter, alternate 32-column chunks
-// TMEM: two accumulators of kTok columns, so a tile's epilogue overlaps the next tile's MMAs, and a set
-// of scales per stage.  Every mbarrier wait is bounded: on timeout the kernel records JMOE_DEV_TIMEOUT in the
-// workspace status word, the other roles stop at their next wait, in-flight copies and MMAs are waited for
-// (bounded), TMEM is released and the CTA returns.
+//   warp 0      codes: TMA boxes of 128 bytes x 128 (dual: 16) weight rows and x 32 or a full tile's token rows
+//   warp 1      TMEM allocator; per stage copies the scales to TMEM (tcgen05.cp) and issues the MMAs, 64 k each.
+//               It stays converged and one elected lane issues (by one lane alone: 2.9 instead of 5.3 TB/s on 128 rows)
+//   4-6 warps   scales: two sets, in turns, of one warp per 128 rows of weights or tokens.  The tensor core wants 512-byte
+//               blocks of 128 rows x 128 k with row r at 16 (r % 32) + 4 (r / 32); a lane reads 32 bytes (a DRAM sector:
+//               1024 of K) of rows lane, lane + 32, + 64, + 96 into registers, ahead of their use and across tiles, and
+//               stores 16 bytes per block.  (One set, half as far ahead: 94 instead of 86 us on 128 rows.)
+//   8 warps     epilogue: two warps per TMEM lane quarter, alternate 16-token units
+// TMEM: two accumulators of kTok columns, so a tile's epilogue overlaps the next tile's MMAs, and sets of scale
+// columns.  Every mbarrier wait is bounded: on timeout the kernel records JMOE_DEV_TIMEOUT in the workspace status
+// word, the other roles stop at their next wait, in-flight copies and MMAs are waited for (bounded), TMEM is released
+// and the CTA returns.
 //
 // Tile order: expert by expert; inside an expert, bands of token tiles whose codes stay in L2 while every
 // weight tile streams past once per band; token tiles fastest, so the CTAs working at the same time share
-// each weight tile.  Tile i of a CTA is its index + i * grid.
+// each weight tile.  CTA (or pair) i of n takes tiles i, i + n, ...: DRAM reads are the operands once (16384 x 14336 x
+// 4096: 535 MB for 534).
+//
+// Measured (random codes; B200, 6.46 TB/s copy, 1.71 PFLOP/s bf16): 128 rows over 16 experts, 14336 x 4096: 81 us,
+// 6.2 TB/s: HBM.  16384 rows: 400-420 us, 4.6-4.8 PFLOP/s, tensor pipe 72 % active; 315 us on constant codes, and
+// 480 us back to back for seconds: the power limit, not the pipeline, sets the pace.  Tried and dropped: the stages of few tiles
+// divided evenly among all CTAs with partial sums through memory (two rows x 4096 x 14336: 18.7 -> 21.1 us, the
+// exchange costs what the balance gains), tiles of 64 weight rows (17.0 -> 19.0 us: the stages' pace, not their
+// bytes, bounds 64 CTAs), a look at the next stage's barrier between a stage's MMAs (414 -> 427 us).
 #include <cuda.h>
 
 #include <atomic>
