@@ -153,6 +153,32 @@ def test_grouped_mixed_scales(counts, rows, cols, dtype):
     assert (np.abs(y - want) <= tol).all(), np.max(np.abs(y - want) / tol)
 
 
+@pytest.mark.parametrize("counts,rows,cols", [([2], 40, 32768), ([70], 40, 32768), ([3, 1], 65536, 128), ([0, 200], 65535, 256)])
+def test_grouped_largest_sizes(counts, rows, cols):
+    # sums of at most 32768 terms that are multiples of 1/4 and below 36: 4 * 36 * 2^15 < 2^23
+    rng = np.random.default_rng(cols)
+    x, w = operands(rng, sum(counts), rows, cols, len(counts), [127])
+    y = run_grouped(x, w, offsets_of(counts)).cpu().numpy()
+    assert np.array_equal(y, ref.grouped(ref.values(*x), offsets_of(counts), ref.values(*w))[0])
+
+
+@pytest.mark.parametrize("n", [30, 400])  # single CTAs, pairs
+def test_grouped_operands_off_32_bytes(n):
+    """Scales on 4-byte, codes and results on 16-byte boundaries only, at a K whose scales could be read 32 bytes at a time."""
+    rng = np.random.default_rng(n)
+    x, w = operands(rng, n, 72, 2048, 1, [127, 128])
+
+    def shifted(a, by):
+        t = torch.zeros(a.size + by, dtype=torch.uint8, device="cuda")[by:].view(a.shape)
+        return t.copy_(cuda(a))
+
+    off = cuda(np.array([0, n], np.int32))
+    want = ref.grouped(ref.values(*x), [0, n], ref.values(*w))[0]
+    y = torch.zeros(n * 72 + 8, dtype=torch.bfloat16, device="cuda")[8:].view(n, 72)
+    jm.jamba_moe_grouped_mx4(shifted(x[0], 16), shifted(x[1], 4), off, shifted(w[0], 48), shifted(w[1], 20), y=y)
+    assert np.array_equal(dev_to_bf16_bits(y), ref.bf16_bits(want))
+
+
 def test_grouped_far_scales():
     # x near the top of the scales' range, w near its bottom: the products are ordinary numbers
     rng = np.random.default_rng(8)
@@ -376,6 +402,34 @@ def test_layer_wait_runs_out(T):
         jm.jamba_moe_debug_skip_copy(False)
     assert torch.equal(L.forward(workspace=ws)[0], want)
     assert jm.jamba_moe_read_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("T", [20, 600])
+def test_layer_captured(T):
+    """Two graphs of the layer that share one workspace, replayed in turn, follow their inputs."""
+    a, b = Layer(T, 256, 384), Layer(T, 256, 384)
+    b.x = synth.f32_to_bf16_bits(-synth.bf16_bits_to_f32(a.x))
+    want = [L.forward()[0] for L in (a, b)]
+    ws = torch.empty(jm.jamba_moe_workspace_size_mx4(T, 256, 384), dtype=torch.uint8, device="cuda")
+    wr = torch.from_numpy(a.wr).cuda()
+    bias = None if a.bias is None else cuda(a.bias)
+    side = torch.cuda.Stream()
+    graphs, outs, xs = [], [], [bf16_to_dev(L.x) for L in (a, b)]
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for L, x in zip((a, b), xs):
+            y = torch.zeros(T, 256, dtype=torch.bfloat16, device="cuda")
+            ids, w = torch.zeros(T, 2, dtype=torch.int32, device="cuda"), torch.zeros(T, 2, device="cuda")
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                jm.jamba_moe_forward_mx4(x, wr, bias, *L.dev, y=y, topk_ids=ids, topk_w=w, workspace=ws)
+            graphs.append(g)
+            outs.append((y, ids, w))
+        for k in (0, 1, 1, 0):
+            graphs[k].replay()
+            side.synchronize()
+            assert torch.equal(outs[k][0], want[k]) and jm.jamba_moe_read_device_status(ws, stream=side) == 0
+            outs[k][0].zero_()
 
 
 def test_layer_no_tokens():

@@ -118,6 +118,92 @@ def test_binding_refusals():
         jm.jamba_moe_quantize_mx4(np.zeros((4, 64)))
 
 
+class FakeStream:
+    def __init__(self, device, handle=0x5151):
+        self.device, self.cuda_stream = device, handle
+
+
+@pytest.fixture
+def fake(monkeypatch, lib):
+    """A stand-in library that records its calls, checked against the declared argument lists; tensors on the CPU
+    stand for the device's, `fake.current` is the current device's index."""
+    import contextlib
+
+    import torch
+
+    class Recorder:
+        calls, devices, current = [], [], 7
+
+        def __getattr__(self, name):
+            declared = getattr(lib, name).argtypes
+
+            def call(*args):
+                assert len(args) == len(declared), name
+                self.calls.append((name, args))
+                return 4096 if "workspace_size" in name else 0
+
+            return call
+
+    rec = Recorder()
+    rec.calls, rec.devices = [], []
+
+    @contextlib.contextmanager
+    def switched(dev):
+        rec.devices.append(dev)
+        yield
+
+    monkeypatch.setattr(jm, "_lib", rec)
+    monkeypatch.setattr(jm, "_check", lambda *a, **k: None)
+    monkeypatch.setattr(torch.cuda, "device", switched)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: rec.current)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: FakeStream(dev))
+    monkeypatch.setattr(jm, "_current_raw_stream", lambda index: 0x7777)
+    return rec
+
+
+def test_binding_marshals_and_switches_devices(fake):
+    import torch
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)  # noqa: E731
+    xq, xs, Q, S = u8(5, 64), u8(5, 4), u8(3, 40, 64), u8(3, 40, 4)
+    off = torch.zeros(4, dtype=torch.int32)
+    for current, stream in ((7, 0x5151), (None, 0x7777)):  # another device is current; the tensors' own is
+        fake.current = current
+        fake.calls.clear()
+        q, s = jm.jamba_moe_quantize_mx4(torch.zeros(2, 3, 64, dtype=torch.bfloat16))
+        assert tuple(q.shape) == (2, 3, 32) and tuple(s.shape) == (2, 3, 2) and q.dtype == s.dtype == torch.uint8
+        w = jm.jamba_moe_dequantize_mx4(q, s)
+        assert tuple(w.shape) == (2, 3, 64) and w.dtype == torch.bfloat16
+        y = jm.jamba_moe_grouped_mx4(xq, xs, off, Q, S, out_dtype=torch.float32)
+        assert tuple(y.shape) == (5, 40) and y.dtype == torch.float32
+        out = jm.jamba_moe_forward_mx4(torch.zeros(4, 128, dtype=torch.bfloat16), torch.zeros(16, 128), None,
+                                       u8(16, 256, 64), u8(16, 256, 4), u8(16, 256, 64), u8(16, 256, 4),
+                                       u8(16, 128, 128), u8(16, 128, 8))
+        assert [tuple(t.shape) for t in out] == [(4, 128), (4, 2), (4, 2)]
+        calls = [(n, a) for n, a in fake.calls if "workspace_size" not in n]
+        assert [n for n, _ in calls] == ["jamba_moe_quantize_mx4", "jamba_moe_dequantize_mx4", "jamba_moe_grouped_mx4",
+                                         "jamba_moe_forward_mx4"]
+        assert calls[0][1][1:4] == (2, 3, 64) and calls[1][1][2:5] == (2, 3, 64)
+        assert calls[2][1][3:7] == (5, 40, 128, 3) and calls[2][1][10] == jm.OUT_FP32
+        assert calls[3][1][9:14] == (4, 128, 256, 16, 2)
+        assert all(a[-1] == stream for _, a in calls)
+    assert fake.devices == [torch.device("cpu")] * 4  # switched for the first four calls only
+
+
+def test_binding_refuses_mixed_devices_and_streams(fake):
+    import torch
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)  # noqa: E731
+    args = [u8(5, 64), u8(5, 4), torch.zeros(4, dtype=torch.int32), u8(3, 40, 64), u8(3, 40, 4)]
+    with pytest.raises(ValueError, match="S is on meta"):
+        jm.jamba_moe_grouped_mx4(*args[:4], args[4].to("meta"))
+    with pytest.raises(ValueError, match="stream belongs to"):
+        jm.jamba_moe_grouped_mx4(*args, stream=FakeStream(torch.device("meta")))
+    with pytest.raises(TypeError, match="out_dtype"):
+        jm.jamba_moe_grouped_mx4(*args, out_dtype=torch.float16)
+    with pytest.raises(ValueError, match="xq must be"):
+        jm.jamba_moe_grouped_mx4(args[0][None], *args[1:])
+    assert not [n for n, _ in fake.calls if n == "jamba_moe_grouped_mx4"]
+
+
 def test_kernel_names(lib):
     lib.jamba_moe_kernel_name.restype = ctypes.c_char_p
     assert [lib.jamba_moe_kernel_name(k).decode() for k in range(len(jm.KERNEL_NAMES))] == jm.KERNEL_NAMES
