@@ -24,11 +24,11 @@
 // or, where each tile has few tokens, 512:
 //   warp 0      codes: TMA boxes of 128 bytes x 128 (dual: 16) weight rows and x 32 or a full tile's token rows
 //   warp 1      TMEM allocator; per stage copies the scales to TMEM (tcgen05.cp) and issues the MMAs, 64 k each.
-//               It stays converged and one elected lane issues (by one lane alone: 2.9 instead of 5.3 TB/s on 128 rows)
-//   4-6 warps   scales: two sets, in turns, of one warp per 128 rows of weights or tokens.  The tensor core wants 512-byte
-//               blocks of 128 rows x 128 k with row r at 16 (r % 32) + 4 (r / 32); a lane reads 32 bytes (a DRAM sector:
-//               1024 of K) of rows lane, lane + 32, + 64, + 96 into registers, ahead of their use and across tiles, and
-//               stores 16 bytes per block.  (One set, half as far ahead: 94 instead of 86 us on 128 rows.)
+//   4-6 warps   scales: two sets, in turns, of one warp per 128 rows of weights or tokens.  The tensor core wants
+//               512-byte blocks of 128 rows x 128 k with row r at 16 (r % 32) + 4 (r / 32); a lane reads 32 bytes (a
+//               DRAM sector: 1024 of K) of rows lane, lane + 32, + 64, + 96 into registers, ahead of their use and
+//               across tiles, and stores 16 bytes per block.  (One set, half as far ahead: 94 instead of 86 us on 128
+//               rows.)
 //   8 warps     epilogue: two warps per TMEM lane quarter, alternate 16-token units
 // TMEM: two accumulators of kTok columns, so a tile's epilogue overlaps the next tile's MMAs, and sets of scale
 // columns.  Every mbarrier wait is bounded: on timeout the kernel records JMOE_DEV_TIMEOUT in the workspace status
@@ -42,9 +42,9 @@
 //
 // Measured (random codes; B200, 6.46 TB/s copy, 1.71 PFLOP/s bf16): 128 rows over 16 experts, 14336 x 4096: 81 us,
 // 6.2 TB/s: HBM.  16384 rows: 400-420 us, 4.6-4.8 PFLOP/s, tensor pipe 72 % active; 315 us on constant codes, and
-// 480 us back to back for seconds: the power limit, not the pipeline, sets the pace.  Tried and dropped: the stages of few tiles
-// divided evenly among all CTAs with partial sums through memory (two rows x 4096 x 14336: 18.7 -> 21.1 us, the
-// exchange costs what the balance gains), tiles of 64 weight rows (17.0 -> 19.0 us: the stages' pace, not their
+// 480 us back to back for seconds: the power limit, not the pipeline, sets the pace.  Tried and dropped: the stages of
+// few tiles divided evenly among all CTAs with partial sums through memory (two rows x 4096 x 14336: 18.7 -> 21.1 us,
+// the exchange costs what the balance gains), tiles of 64 weight rows (17.0 -> 19.0 us: the stages' pace, not their
 // bytes, bounds 64 CTAs), a look at the next stage's barrier between a stage's MMAs (414 -> 427 us).
 #include <cuda.h>
 
@@ -63,7 +63,7 @@ constexpr int kWRows = 128;
 constexpr int kSubBytes = 128;    // bytes of codes per row and sub-step: 256 of K
 constexpr int kBoxRows = 32;      // token rows per copy
 constexpr int kEpiWarps = 8;
-constexpr int kOutPitch = 80;     // bytes per token of a warp's 16-token staging area (32 bf16, plus 16: no bank conflicts)
+constexpr int kOutPitch = 80;     // bytes per token of a warp's 16-token staging area (32 bf16, and no bank conflicts)
 constexpr int kOutBytes = 16 * kOutPitch;
 constexpr int kSfWords = 8;       // words of scales that a lane holds of each of its rows: 32 bytes
 constexpr uint32_t kMaxPolls = 1u << 22;      // ~0.3 s of polling: far above any healthy wait
@@ -97,7 +97,11 @@ struct Cfg {
     static constexpr int kBars = 2 * kStages + 5;
     static constexpr int kSmem = kStages * kStage + kEpiWarps * kOutBytes + 1024 + 8 * kBars;
     static_assert(kThreads >= kMaxGroups, "one thread per group");
-    static_assert(kTok % 16 == 0 && kB % 1024 == 0 && kStages >= 3 && kSfSets >= 2, "tile");
+    static_assert(kTok % 16 == 0 && kB % 1024 == 0 && kSfSets >= 2, "tile");
+    // A set of scale warps waits for stage g - kSfSets to be consumed and knows, from its last turn, that stage
+    // g - kSfStages - 1 - kSfSets was: a barrier's parity says the right thing only if that is not before
+    // g - kSfSets - kStages.
+    static_assert(kStages > kSfStages, "scale warps would run a round ahead of the barrier they wait on");
 };
 
 struct Tile {
@@ -165,13 +169,13 @@ __device__ __forceinline__ void fail(WsHeader* hdr, volatile int* abort) {
 // v (see tmem_ld_16x16; lanes 0-15, then 16-31) go transposed through the warp's area `out` of shared memory and
 // leave as 16-byte pieces of y rows, element by element where rows are no multiple of 8 long.  (Trading values
 // between neighbouring lanes and storing 4 bytes each took 1200 cycles per 16 tokens.)
-__device__ __forceinline__ void store_bf16(const Args& p, uint32_t out, const uint32_t (&v)[16], int64_t row0, int n, int j0,
-                                           int lane) {
+__device__ __forceinline__ void store_bf16(const Args& p, uint32_t out, const uint32_t (&v)[16], int64_t row0, int n,
+                                           int j0, int lane) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)  // 4 j blocks of 8, for each of two token blocks
-        tc::stmatrix_x4_trans(out + (8 * i + (lane & 7)) * kOutPitch + 16 * (lane >> 3), pack_bf16(v[4 * i], v[4 * i + 1]),
-                              pack_bf16(v[4 * i + 2], v[4 * i + 3]), pack_bf16(v[8 + 4 * i], v[9 + 4 * i]),
-                              pack_bf16(v[10 + 4 * i], v[11 + 4 * i]));
+        tc::stmatrix_x4_trans(out + (8 * i + (lane & 7)) * kOutPitch + 16 * (lane >> 3),
+                              pack_bf16(v[4 * i], v[4 * i + 1]), pack_bf16(v[4 * i + 2], v[4 * i + 3]),
+                              pack_bf16(v[8 + 4 * i], v[9 + 4 * i]), pack_bf16(v[10 + 4 * i], v[11 + 4 * i]));
     __syncwarp();
     uint16_t* y = p.y16 + row0 * p.M + j0;
     if (p.M % 8 == 0) {
@@ -201,16 +205,18 @@ __device__ __forceinline__ uint4 swiglu_bf16(uint32_t out, const uint32_t (&v)[1
     for (int i = 0; i < 4; ++i)  // 2 j blocks x 2 token blocks of 8
         m[i] = pack_bf16(silu_fast(__uint_as_float(v[2 * i])) * __uint_as_float(v[8 + 2 * i]),
                          silu_fast(__uint_as_float(v[2 * i + 1])) * __uint_as_float(v[9 + 2 * i]));
-    tc::stmatrix_x4_trans(out + (8 * (lane >> 4) + (lane & 7)) * kPitch + 16 * ((lane >> 3) & 1), m[0], m[1], m[2], m[3]);
+    tc::stmatrix_x4_trans(out + (8 * (lane >> 4) + (lane & 7)) * kPitch + 16 * ((lane >> 3) & 1), m[0], m[1], m[2],
+                          m[3]);
     __syncwarp();
     const uint4 q = ld_shared_v4(out + (lane >> 1) * kPitch + 16 * (lane & 1));
     __syncwarp();  // the area is rewritten by the next 16 tokens
     return q;
 }
 
-// 16 tokens (the first n of them live) of column j as fp32: y rows row0 .., or, times their routing weights, the slots of
-// their assignments.
-__device__ __forceinline__ void store_fp32(const Args& p, const uint32_t (&v)[16], int64_t row0, int n, int j, int lane) {
+// 16 tokens (the first n of them live) of column j as fp32: y rows row0 .., or, times their routing weights, the slots
+// of their assignments.
+__device__ __forceinline__ void store_fp32(const Args& p, const uint32_t (&v)[16], int64_t row0, int n, int j,
+                                           int lane) {
     if (p.wts) {
         const int32_t a_l = lane < min(n, 16) ? p.perm[row0 + lane] : -1;
         const float w_l = a_l >= 0 ? p.wts[a_l] : 0.0f;
@@ -292,10 +298,10 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
     if (first >= total) return;  // no tile for this CTA (or pair): nothing was taken yet
 
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* sA = smem;                          // [kStages][128 rows][128 B]
-    uint8_t* sB = sA + kStages * C::kA;          // [kStages][kTok rows][128 B]
-    uint8_t* sSA = sB + kStages * C::kB;         // [kStages][2][512 B]
-    uint8_t* sSB = sSA + kStages * C::kSfA;      // [kStages][2][kSfBlocks][512 B]
+    uint8_t* sA = smem;                          // [kStages][kSub][128 rows][128 B]
+    uint8_t* sB = sA + kStages * C::kA;          // [kStages][kSub][kTokCta rows][128 B]
+    uint8_t* sSA = sB + kStages * C::kB;         // [kStages][kWords][512 B]
+    uint8_t* sSB = sSA + kStages * C::kSfA;      // [kStages][kWords][kSfBlocks][512 B]
     uint8_t* sOut = sSB + kStages * C::kSfB;     // [kEpiWarps][16 tokens][kOutPitch]
     uint64_t* full = reinterpret_cast<uint64_t*>(sOut + kEpiWarps * kOutBytes);  // [kStages] codes and scales are there
     uint64_t* empty = full + kStages;            // [kStages] MMAs reading the stage are done
@@ -341,8 +347,15 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
         if (!abort_flag) fail(p.hdr, &abort_flag);
         return false;
     };
-    // Arrive on the barrier of the CTA that issues the MMAs.  What it then starts in this CTA (its tensor core
-    // reading this CTA's scales, or overwriting the accumulator) is ordered after this thread's own proxy or tcgen05 fence.
+    // The same outcome for all lanes of a warp, where what follows needs them together.
+    auto wait_warp = [&](uint64_t* bar, int round) -> bool { return __all_sync(0xffffffffu, wait(bar, round)); };
+    // The two issuing warps: every lane walks the loop and waits, one elected lane issues.  Inside a tile nothing needs
+    // the lanes together (one may give up alone); after each tile they agree whether to go on.  (Lane 0 as the issuer,
+    // in place of an elected lane: 570 instead of 425 us for the large product; only the issuing lane in the loop:
+    // 485; a vote on each wait: 450.)
+    const bool lead = tc::elect_one();
+    // Arrive on the barrier of the CTA that issues the MMAs.  What it then starts in this CTA (its tensor core reading
+    // this CTA's scales, or overwriting the accumulator) is ordered after this thread's own proxy or tcgen05 fence.
     auto arrive = [&](uint64_t* bar) {
         if constexpr (kPair)
             tc::mbar_arrive_cluster(tc::map_to_cta(tc::smem_u32(bar), 0));
@@ -356,7 +369,7 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
         int g = 0;
         bool ok = true;
         Tile t;
-        for (int L = first; ok && L < total; L += stride) {
+        for (int L = first; L < total; L += stride) {
             tile_at<kTok>(G, p, L, t);
             const int w_row0 = t.e * p.M + (t.n * C::kCtas + rank) * kRowsCta;
             const int part = ((t.ntok + 15) & ~15) / C::kCtas;  // this CTA's token rows
@@ -369,7 +382,7 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
                 if (r > 0 && !(ok = wait(&empty[s], r - 1))) break;
                 if (p.skip_copy && blockIdx.x == 0 && g == 1) continue;
                 const int n_sub = min(C::kSub, (KW - kb * kWords + 1) / 2);
-                if (tc::elect_one()) {
+                if (lead) {
                     if (rank == 0) tc::mbar_arrive_expect_tx(&full[s], n_sub * sub_bytes);
                     for (int sub = 0; sub < n_sub; ++sub) {
                         const int x = (kb * C::kSub + sub) * kSubBytes;
@@ -391,12 +404,13 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
                             load(da, &tmW0, w_row0);
                         }
                         if (n_box == 0) load(db, &tmX, x_row0);
-                        for (int i = 0; i < n_box; ++i) load(db + i * kBoxRows * kSubBytes, &tmXs, x_row0 + i * kBoxRows);
+                        for (int i = 0; i < n_box; ++i)
+                            load(db + i * kBoxRows * kSubBytes, &tmXs, x_row0 + i * kBoxRows);
                     }
                 }
-                __syncwarp();
                 issued = g + 1;
             }
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
         }
         // the last stages' arrivals come from the other CTA: they have to be here before this one may end
         if (kPair)
@@ -409,7 +423,8 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
         const uint32_t dst0 = tc::smem_u32(blk < 0 ? sSA : sSB + 512 * blk) + 16 * lane;
         const uint32_t dst_stage = blk < 0 ? C::kSfA : C::kSfB;
         const uint32_t dst_word = blk < 0 ? 512 : 512 * C::kSfBlocks;
-        // what is loaded next: rows 32 i + lane (i < live) of tile L, from the tile's stage kb, this CTA's stage g_load, on
+        // what is loaded next: rows 32 i + lane (i < live) of tile L, from the tile's stage kb on, which is this CTA's
+        // stage g_load
         const uint8_t* ptr[4] = {};
         int L = first, kb = 0, g_load = 0, live = 0, opened = -1;
         Tile t;
@@ -461,14 +476,15 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
 #pragma unroll
             for (int st = 0; st < kSfStages; ++st) {
                 if (st >= n) break;
-                const int s = (g + st) % kStages, r = (g + st) / kStages;
-                const bool free_ = r == 0 || wait(&empty[s], r - 1);
-                if (!(ok = __all_sync(0xffffffffu, free_))) break;
+                // the stage's place in shared memory is free, and so are its scale columns in TMEM, of which there may
+                // be fewer sets than stages: the issuer need not look after those
+                const int s = (g + st) % kStages, before = g + st - C::kSfSets;
+                if (!(ok = before < 0 || wait_warp(&empty[before % kStages], before / kStages))) break;
 #pragma unroll
                 for (int w = 0; w < kWords; ++w)
                     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst0 + s * dst_stage + w * dst_word),
-                                 "r"(cur[0][kWords * st + w]), "r"(cur[1][kWords * st + w]), "r"(cur[2][kWords * st + w]),
-                                 "r"(cur[3][kWords * st + w])
+                                 "r"(cur[0][kWords * st + w]), "r"(cur[1][kWords * st + w]),
+                                 "r"(cur[2][kWords * st + w]), "r"(cur[3][kWords * st + w])
                                  : "memory");
                 tc::fence_proxy_async_smem();
                 __syncwarp();
@@ -482,8 +498,9 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
             g = g_next;
         }
     } else if (warp == 1 && rank == 0) {
-        // ---------------- MMA issuer: the warp stays converged, one elected lane issues
-        const uint64_t adesc0 = tc::sw128_kmajor_desc(tc::smem_u32(sA)), bdesc0 = tc::sw128_kmajor_desc(tc::smem_u32(sB));
+        // ---------------- MMA issuer
+        const uint64_t adesc0 = tc::sw128_kmajor_desc(tc::smem_u32(sA));
+        const uint64_t bdesc0 = tc::sw128_kmajor_desc(tc::smem_u32(sB));
         const uint64_t sadesc0 = tc::linear_desc(tc::smem_u32(sSA)), sbdesc0 = tc::linear_desc(tc::smem_u32(sSB));
         auto commit = [](uint64_t* bar) {
             if constexpr (kPair)
@@ -500,19 +517,16 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
             const uint32_t idesc0 = tc::idesc_mx4_f32(C::kCtas * kWRows, n_mma, 0);
             const uint32_t idesc2 = tc::idesc_mx4_f32(C::kCtas * kWRows, n_mma, 2);
             const int buf = it & 1, u = it >> 1;
-            if (u > 0 && !(ok = wait(&acc_empty[buf], u - 1))) break;
+            if (u > 0 && !(ok = wait_warp(&acc_empty[buf], u - 1))) break;
             const uint32_t d_tmem = tmem + (uint32_t)(buf * kTok);
             for (int kb = 0; kb < KB; ++kb, ++g) {
                 const int s = g % kStages, r = g / kStages;
                 if (!(ok = wait(&full[s], r))) break;
-                // fewer sets of scale columns than stages: the MMAs that read this set last have to be done
-                if (C::kSfSets < kStages && g >= C::kSfSets &&
-                    !(ok = wait(&empty[(g - C::kSfSets) % kStages], (g - C::kSfSets) / kStages)))
-                    break;
                 tc::tc_fence_after();
-                if (tc::elect_one()) {
+                if (lead) {
                     const uint32_t sf = tmem + C::kSfCol0 + (uint32_t)(g % C::kSfSets * C::kSfCols);
-                    const uint64_t adesc = adesc0 + (uint32_t)(s * (C::kA >> 4)), bdesc = bdesc0 + (uint32_t)(s * (C::kB >> 4));
+                    const uint64_t adesc = adesc0 + (uint32_t)(s * (C::kA >> 4));
+                    const uint64_t bdesc = bdesc0 + (uint32_t)(s * (C::kB >> 4));
                     const uint64_t sadesc = sadesc0 + (uint32_t)(s * (C::kSfA >> 4));
                     const uint64_t sbdesc = sbdesc0 + (uint32_t)(s * (C::kSfB >> 4));
                     // 512 bytes = +32 in a descriptor's address field; a last stage need not hold all words
@@ -539,12 +553,11 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
                     commit(&empty[s]);
                     if (kb == KB - 1) commit(&acc_full[buf]);
                 }
-                __syncwarp();
                 issued = g + 1;
             }
-            if (!ok) break;
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
         }
-        if (!ok && tc::elect_one()) commit(mma_done);  // arrives once every MMA issued above has completed
+        if (!ok && lead) commit(mma_done);  // arrives once every MMA issued above has completed
         __syncwarp();
     } else if (warp >= kEpiWarp0) {
         // ---------------- epilogue, 16 tokens at a time
@@ -555,9 +568,10 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
         for (int L = first; L < total; L += stride, ++it) {
             tile_at<kTok>(G, p, L, t);
             const int b = it & 1, u = it >> 1;
-            bool ok = wait(&acc_full[b], u);
-            if constexpr (kDual) ok = !tc::named_sync_or(1 + (ew >> 1), 64, !ok);  // the two warps stop together or not at all
-            if (!__all_sync(0xffffffffu, ok)) break;  // tcgen05.ld below is warp-collective
+            bool ok = wait_warp(&acc_full[b], u);
+            // the two warps that trade magnitudes stop together or not at all
+            if constexpr (kDual) ok = !tc::named_sync_or(1 + (ew >> 1), 64, !ok);
+            if (!ok) break;
             tc::tc_fence_after();
             const uint32_t t_lane = tmem + ((uint32_t)(32 * qd) << 16) + (uint32_t)(b * kTok);
             const uint32_t out = tc::smem_u32(sOut + ew * kOutBytes);
@@ -620,15 +634,17 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
     tc::tc_fence_before();
     __syncthreads();
     if (abort_flag) {
-        if (warp == 0 && lane == 0 && rank == 0) {
+        if (warp == 0 && lead && rank == 0) {
             for (int s = 0; s < kStages; ++s) {
                 if (s >= issued) continue;
                 const int last = (issued - 1 - s) / kStages;
-                // a copy of round r completes phase `last` of full[s] once the scales are there too, else this wait runs out
+                // a copy of round r completes phase `last` of full[s] once the scales are there too; else this wait
+                // runs out, long after the copy has landed
                 for (uint32_t i = 0; i < p.max_polls && !tc::mbar_try_wait(&full[s], last & 1); ++i) __nanosleep(64);
             }
         }
-        if (warp == 1 && lane == 0) {  // completes if the issuer gave up; if it did not, its last MMAs are long done after this
+        // completes if the issuer gave up; if it did not, its last MMAs are long done after this
+        if (warp == 1 && lead) {
             for (uint32_t i = 0; i < p.max_polls && !tc::mbar_try_wait(mma_done, 0); ++i) __nanosleep(64);
         }
         __syncthreads();
@@ -731,9 +747,10 @@ cudaError_t launch(Args p, cudaStream_t st, int num_sms) {
 
 cudaError_t launch_grouped_mx4(const mx4::Args& p, cudaStream_t st, int num_sms) {
     using namespace mx4;
-    // Few rows per expert: single CTAs with narrow token tiles, whose stages are the weights in flight; else pairs.  Single
-    // or pairs, us, 14336 x 4096 weights of 16 experts, by rows of each: 4: 79 / 84, 48: 85 / 89, 64: 86 / 90, 96: 104 / 94,
-    // 128: 120 / 97.  A group over 64 rows takes two narrow tiles, and uneven groups reach that at a mean of 48.
+    // Few rows per expert: single CTAs with narrow token tiles, whose stages are the weights in flight; else pairs.
+    // Single or pairs, us, 14336 x 4096 weights of 16 experts, by rows of each: 4: 79 / 84, 48: 85 / 89, 64: 86 / 90,
+    // 96: 104 / 94, 128: 120 / 97.  A group over 64 rows takes two narrow tiles, and uneven groups reach that at a mean
+    // of 48.
     const bool few = p.rows <= (int64_t)48 * p.E;
     if (p.qb) return few ? launch<true, false, 64>(p, st, num_sms) : launch<true, true, 208>(p, st, num_sms);
     return few ? launch<false, false, 64>(p, st, num_sms) : launch<false, true, 208>(p, st, num_sms);

@@ -174,7 +174,8 @@ static unsigned mx_blocks(int64_t chunks, int num_sms, int per_sm) {
 // elements % 32 == 0.
 cudaError_t launch_quantize_mx4(const uint16_t* W, int64_t elements, uint8_t* Q, uint8_t* S, cudaStream_t st,
                                 int num_sms) {
-    const auto kernel = reinterpret_cast<uintptr_t>(W) % 32 == 0 ? quantize_mx4_kernel<true> : quantize_mx4_kernel<false>;
+    const auto kernel =
+        reinterpret_cast<uintptr_t>(W) % 32 == 0 ? quantize_mx4_kernel<true> : quantize_mx4_kernel<false>;
     return launch_pdl(kernel, dim3(mx_blocks(elements / 16, num_sms, 64)), dim3(kMxThreads), 0, st, W,
                       elements / 16, Q, S);
 }

@@ -127,8 +127,8 @@ __device__ __forceinline__ void fence_proxy_async_smem() { asm volatile("fence.p
 // Four 8 x 8 matrices of 16-bit elements, transposed, to shared memory: lane l holds elements (l / 4, 2 (l % 4)) and
 // the next of each; lane 8 m + c gives the address of the 16 bytes that receive column c of matrix m.
 __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t m0, uint32_t m1, uint32_t m2, uint32_t m3) {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared::cta.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(m0), "r"(m1),
-                 "r"(m2), "r"(m3)
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared::cta.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(m0),
+                 "r"(m1), "r"(m2), "r"(m3)
                  : "memory");
 }
 
@@ -301,9 +301,9 @@ __device__ __forceinline__ uint64_t linear_desc(uint32_t smem_addr) {
 }
 
 // Instruction descriptor for kind::mxf4: E2M1 A and B, both K-major, E8M0 scales, fp32 D, shape M x N
-// (M = 128, or 256 for a pair of CTAs).  A 32-bit TMEM cell holds four consecutive scales of one row (k blocks of 32); row r is in
-// lane r % 32 (of every quarter), column r / 32.  An instruction (two blocks) takes the scales in bytes
-// `pair` and pair + 1 of the cells, pair = 0 or 2.
+// (M = 128, or 256 for a pair of CTAs).  A 32-bit TMEM cell holds four consecutive scales of one row
+// (k blocks of 32); row r is in lane r % 32 (of every quarter), column r / 32.  An instruction (two
+// blocks) takes the scales in bytes `pair` and pair + 1 of the cells, pair = 0 or 2.
 __host__ __device__ constexpr uint32_t idesc_mx4_f32(int M, int N, int pair) {
     return ((uint32_t)pair << 4)            // B scale byte
            | (1u << 7)                      // A format: E2M1

@@ -121,7 +121,8 @@ def offsets_of(counts):
 SHAPES = [
     ([1], 1, 128), ([1], 128, 256), ([0, 1, 0], 129, 384), ([16, 17], 127, 128), ([31, 33, 32], 130, 512),
     ([64, 65, 0, 63], 256, 640), ([223, 224, 225], 100, 256), ([255, 0, 257, 1], 384, 384), ([449], 131, 128),
-    ([1000], 64, 256), ([0, 0, 0, 700], 257, 512), ([3] * 100, 65, 256), ([2, 0] * 128, 40, 128), ([5] * 17, 1411, 2176),
+    ([1000], 64, 256), ([0, 0, 0, 700], 257, 512), ([3] * 100, 65, 256), ([2, 0] * 128, 40, 128),
+    ([5] * 17, 1411, 2176),
     ([1500, 40], 640, 1024), ([207, 208, 209], 255, 256), ([416, 417], 257, 1024), ([96, 97, 161, 160, 113], 129, 1152),
     ([1], 1, 2048), ([40], 128, 14336), ([1, 1], 300, 4224), ([48, 0, 48, 47, 5], 777, 3968), ([33], 64, 16384),
 ]
@@ -153,7 +154,8 @@ def test_grouped_mixed_scales(counts, rows, cols, dtype):
     assert (np.abs(y - want) <= tol).all(), np.max(np.abs(y - want) / tol)
 
 
-@pytest.mark.parametrize("counts,rows,cols", [([2], 40, 32768), ([70], 40, 32768), ([3, 1], 65536, 128), ([0, 200], 65535, 256)])
+@pytest.mark.parametrize("counts,rows,cols", [([2], 40, 32768), ([70], 40, 32768), ([3, 1], 65536, 128),
+                                              ([0, 200], 65535, 256)])
 def test_grouped_largest_sizes(counts, rows, cols):
     # sums of at most 32768 terms that are multiples of 1/4 and below 36: 4 * 36 * 2^15 < 2^23
     rng = np.random.default_rng(cols)
@@ -164,7 +166,8 @@ def test_grouped_largest_sizes(counts, rows, cols):
 
 @pytest.mark.parametrize("n", [30, 400])  # single CTAs, pairs
 def test_grouped_operands_off_32_bytes(n):
-    """Scales on 4-byte, codes and results on 16-byte boundaries only, at a K whose scales could be read 32 bytes at a time."""
+    """Scales on 4-byte, codes and results on 16-byte boundaries only, at a K whose scales could be read 32 bytes
+    at a time."""
     rng = np.random.default_rng(n)
     x, w = operands(rng, n, 72, 2048, 1, [127, 128])
 
@@ -322,7 +325,8 @@ def test_far_rows_of_a_long_batch():
     off = torch.tensor([0, n - 300, n], dtype=torch.int32, device="cuda")
     y = jm.jamba_moe_grouped_mx4(xq, xs, off, q, s, out_dtype=torch.float32)
     for r, e in ((slice(0, 40), 0), (slice(n - 340, n - 300), 0), (slice(n - 300, n), 1)):
-        want = ref.values(xq[r].cpu().numpy(), xs[r].cpu().numpy()) @ ref.values(q[e].cpu().numpy(), s[e].cpu().numpy()).T
+        xv, wv = ref.values(xq[r].cpu().numpy(), xs[r].cpu().numpy()), ref.values(q[e].cpu().numpy(), s[e].cpu().numpy())
+        want = xv @ wv.T
         assert np.array_equal(y[r].cpu().numpy(), want)
 
 
