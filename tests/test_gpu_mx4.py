@@ -305,6 +305,28 @@ def test_grouped_wait_runs_out(counts):
     assert np.array_equal(y.cpu().numpy(), ref.grouped(ref.values(*x), offsets_of(counts), ref.values(*w))[0])
 
 
+def test_memory_of_calls_on_a_given_stream():
+    """What a call on another stream allocated for itself is not handed out again while that stream is still before it."""
+    rng = np.random.default_rng(16)
+    x, w = operands(rng, 40, 300, 512, 2, [127])
+    args = [cuda(x[0]), cuda(x[1]), cuda(np.array([0, 30, 40], np.int32)), cuda(w[0]), cuda(w[1])]
+    L = Layer(20, 256, 256)
+    fixed = [bf16_to_dev(L.x), torch.from_numpy(L.wr).cuda(), None if L.bias is None else cuda(L.bias), *L.dev]
+    want = jm.jamba_moe_forward_mx4(*fixed)[0]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)  # some 50 ms
+    y = jm.jamba_moe_grouped_mx4(*args, out_dtype=torch.float32, stream=side)
+    z = jm.jamba_moe_forward_mx4(*fixed, stream=side)[0]
+    sizes = [4096, 512, jm.jamba_moe_workspace_size_mx4(20, 256, 256)]
+    others = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(8)]
+    torch.cuda.synchronize()
+    assert all((t == 7).all() for t in others)
+    assert np.array_equal(y.cpu().numpy(), ref.grouped(ref.values(*x), [0, 30, 40], ref.values(*w))[0])
+    assert torch.equal(z, want)
+
+
 def test_grouped_deterministic():
     rng = np.random.default_rng(14)
     x, w = operands(rng, 700, 300, 4096, 4, range(110, 140))
