@@ -40,9 +40,10 @@
 // each weight tile.  CTA (or pair) i of n takes tiles i, i + n, ...: DRAM reads are the operands once (16384 x 14336 x
 // 4096: 535 MB for 534).
 //
-// Measured (random codes; B200, 6.46 TB/s copy, 1.71 PFLOP/s bf16): 128 rows over 16 experts, 14336 x 4096: 81 us,
-// 6.2 TB/s: HBM.  16384 rows: 400-420 us, 4.6-4.8 PFLOP/s, tensor pipe 72 % active; 315 us on constant codes, and
-// 480 us back to back for seconds: the power limit, not the pipeline, sets the pace.  Tried and dropped: the stages of
+// Measured (random codes; B200, 6.46 TB/s copy, 1.71 PFLOP/s bf16): 128 rows over 16 experts, 14336 x 4096: 80 us,
+// 6.2 TB/s: HBM.  16384 rows: 425 us, 4.5 PFLOP/s, tensor pipe 71 % active; 320 us on constant codes (265 of them
+// without the epilogue, 245 without MMAs either: what the copies alone need), and 500 us back to back for seconds:
+// mostly the power limit, less the pipeline, sets the pace.  Tried and dropped: the stages of
 // few tiles divided evenly among all CTAs with partial sums through memory (two rows x 4096 x 14336: 18.7 -> 21.1 us,
 // the exchange costs what the balance gains), tiles of 64 weight rows (17.0 -> 19.0 us: the stages' pace, not their
 // bytes, bounds 64 CTAs), a look at the next stage's barrier between a stage's MMAs (414 -> 427 us).
