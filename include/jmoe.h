@@ -306,7 +306,7 @@ int jamba_moe_debug_skip_copy(int on);
 
 /*
  * jamba_moe_debug_checks — debug checks, off by default.  While `on` is non-zero, every MoE
- * forward call (jamba_moe_forward, _path, _bf16w, _fp8) also launches: at its start, a kernel that
+ * forward call (jamba_moe_forward, _path, _bf16w, _fp8, _mx4) also launches: at its start, a kernel that
  * fills the guard gaps the workspace layout leaves after each of its regions with a canary pattern;
  * after the permutation, a kernel that checks the routing tables (counts sum to T*K, every
  * expert's segment is its count rounded up to 128 rows, each permuted row holds -1 or an

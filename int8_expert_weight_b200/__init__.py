@@ -10,9 +10,10 @@ Functions keep the C names: ``jamba_moe_quantize``, ``jamba_moe_workspace_size``
 weights), ``jamba_moe_quantize_fp8`` / ``jamba_moe_workspace_size_fp8`` / ``jamba_moe_forward_fp8``
 (the FP8 comparator layer), ``jamba_moe_quantize_mx4`` / ``jamba_moe_dequantize_mx4`` /
 ``jamba_moe_grouped_mx4`` / ``jamba_moe_forward_mx4`` and their workspace sizes (microscaled 4-bit
-operands: quantization, the product grouped by expert, the layer), ``jamba_mlp_workspace_size`` / ``jamba_mlp_forward`` (the dense
-ExpertsInt8 MLP), ``jamba_moe_forward_noalloc``, ``jamba_moe_read_device_status``,
-``jamba_moe_status_string``, ``jamba_moe_timing_start``, ``jamba_moe_timing_collect``.
+operands: quantization, the product grouped by expert, the layer), ``jamba_mlp_workspace_size`` /
+``jamba_mlp_forward`` (the dense ExpertsInt8 MLP), ``jamba_moe_forward_noalloc``,
+``jamba_moe_read_device_status``, ``jamba_moe_status_string``, ``jamba_moe_timing_start``,
+``jamba_moe_timing_collect``.
 """
 import ctypes
 import os
@@ -357,7 +358,8 @@ def jamba_moe_forward_fp8(x: torch.Tensor, router_W: torch.Tensor, router_bias: 
 
 
 def jamba_moe_quantize_mx4(W: torch.Tensor, stream: Optional[torch.cuda.Stream] = None,
-                           out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+                           out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None
+                           ) -> Tuple[torch.Tensor, torch.Tensor]:
     """MX4 quantization of bf16 rows [..., rows, cols], cols a multiple of 32 (weights or activations).
     Returns (Q uint8 [..., rows, cols / 2], two E2M1 codes a byte, the even element low;
     S uint8 [..., rows, cols / 32], one E8M0 scale per block of 32)."""
