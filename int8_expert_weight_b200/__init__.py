@@ -5,6 +5,9 @@ the C ABI).  This module only marshals arguments: it checks dtypes, devices and 
 tensors, passes their device pointers and the current CUDA stream, and turns a non-zero status
 into a ``JmoeError``.  PyTorch provides device memory and streams; there is no CPU path.
 
+A call that is given a ``stream`` runs on it and nowhere else: its inputs have to be ready there, the MX4 calls
+allocate from that stream's pool, and another stream that reads the results has to wait for it.
+
 Functions keep the C names: ``jamba_moe_quantize``, ``jamba_moe_workspace_size``,
 ``jamba_moe_forward`` (the ExpertsInt8 MoE layer), ``jamba_moe_forward_bf16w`` (unquantized bf16
 weights), ``jamba_moe_quantize_fp8`` / ``jamba_moe_workspace_size_fp8`` / ``jamba_moe_forward_fp8``
@@ -159,12 +162,22 @@ def _one_device(ref: torch.Tensor, **tensors) -> torch.device:
     return ref.device
 
 
-def _made_here(stream: Optional[torch.cuda.Stream], *tensors: torch.Tensor) -> None:
-    """Tensors that a wrapper allocated (on the current stream) and a call uses on `stream`: their memory is not handed
-    out again before that stream has got past the call, however soon they are dropped."""
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(stream)
+def _empty(ref: torch.Tensor, stream: Optional[torch.cuda.Stream], shape, dtype: torch.dtype,
+           returned: bool = True) -> torch.Tensor:
+    """Memory on `ref`'s device for a call on `stream` (None: the current one).
+
+    It comes from the pool of that very stream, so what was queued on it earlier is all that can still touch the block:
+    the current stream's pool may hand out a block that kernels queued there have yet to read or write, which `stream`
+    does not wait for.  A tensor that is returned is meant for the caller's stream too: once dropped, its memory is not
+    handed out again before the current stream has got past what it was given until then."""
+    if stream is None:
+        return ref.new_empty(shape, dtype=dtype)
+    _stream_ptr(stream, ref.device)  # a stream of another device is refused
+    with torch.cuda.stream(stream):
+        t = ref.new_empty(shape, dtype=dtype)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(ref.device))
+    return t
 
 
 # The current stream's handle without a Stream object around it (2 us a call), where torch has it.
@@ -364,7 +377,6 @@ def jamba_moe_quantize_mx4(W: torch.Tensor, stream: Optional[torch.cuda.Stream] 
     Returns (Q uint8 [..., rows, cols / 2], two E2M1 codes a byte, the even element low;
     S uint8 [..., rows, cols / 32], one E8M0 scale per block of 32)."""
     lib = load_library()
-    made = []  # what is allocated here
     _check(W, "W", torch.bfloat16)
     if W.dim() < 2:
         raise ValueError("W must have at least 2 dims (rows, cols)")
@@ -372,16 +384,14 @@ def jamba_moe_quantize_mx4(W: torch.Tensor, stream: Optional[torch.cuda.Stream] 
     n_mats = W.numel() // (rows * cols) if W.numel() else 0
     q_shape, s_shape = W.shape[:-1] + (cols // 2,), W.shape[:-1] + (cols // 32,)
     if out is None:
-        Q = W.new_empty(q_shape, dtype=torch.uint8)
-        S = W.new_empty(s_shape, dtype=torch.uint8)
-        made += [Q, S]
+        Q = _empty(W, stream, q_shape, torch.uint8)
+        S = _empty(W, stream, s_shape, torch.uint8)
     else:
         Q, S = out
         _check(Q, "Q", torch.uint8, q_shape)
         _check(S, "S", torch.uint8, s_shape)
     dev = _one_device(W, Q=Q, S=S)
     st = _launch(lib.jamba_moe_quantize_mx4, dev, stream, W.data_ptr(), n_mats, rows, cols, Q.data_ptr(), S.data_ptr())
-    _made_here(stream, *made)
     if st != 0:
         raise JmoeError(st, "jamba_moe_quantize_mx4")
     return Q, S
@@ -392,7 +402,6 @@ def jamba_moe_dequantize_mx4(Q: torch.Tensor, S: torch.Tensor, out: Optional[tor
     """The values of MX4 codes Q uint8 [..., rows, cols / 2] and scales S uint8 [..., rows, cols / 32]
     as bf16 [..., rows, cols], exact."""
     lib = load_library()
-    made = []  # what is allocated here
     _check(Q, "Q", torch.uint8)
     if Q.dim() < 2:
         raise ValueError("Q must have at least 2 dims (rows, cols / 2)")
@@ -401,14 +410,12 @@ def jamba_moe_dequantize_mx4(Q: torch.Tensor, S: torch.Tensor, out: Optional[tor
     n_mats = Q.numel() // (rows * (cols // 2)) if Q.numel() else 0
     w_shape = Q.shape[:-1] + (cols,)
     if out is None:
-        out = Q.new_empty(w_shape, dtype=torch.bfloat16)
-        made += [out]
+        out = _empty(Q, stream, w_shape, torch.bfloat16)
     else:
         _check(out, "out", torch.bfloat16, w_shape)
     dev = _one_device(Q, S=S, out=out)
     st = _launch(lib.jamba_moe_dequantize_mx4, dev, stream, Q.data_ptr(), S.data_ptr(), n_mats, rows, cols,
                  out.data_ptr())
-    _made_here(stream, *made)
     if st != 0:
         raise JmoeError(st, "jamba_moe_dequantize_mx4")
     return out
@@ -430,7 +437,6 @@ def jamba_moe_grouped_mx4(xq: torch.Tensor, xs: torch.Tensor, offsets: torch.Ten
     torch.float32); rows that belong to no expert are left as they were (unset if y is not given).
     ``workspace`` (uint8, >= jamba_moe_grouped_mx4_workspace_size bytes) is allocated when not given."""
     lib = load_library()
-    made = []  # what is allocated here
     _check(xq, "xq", torch.uint8)
     _check(Q, "Q", torch.uint8)
     if xq.dim() != 2 or Q.dim() != 3:
@@ -444,23 +450,20 @@ def jamba_moe_grouped_mx4(xq: torch.Tensor, xs: torch.Tensor, offsets: torch.Ten
     _check(S, "S", torch.uint8, (E, rows, cols // 32))
     _check(offsets, "offsets", torch.int32, (E + 1,))
     if y is None:
-        y = xq.new_empty((N, rows), dtype=out_dtype)
-        made += [y]
+        y = _empty(xq, stream, (N, rows), out_dtype)
     else:
         _check(y, "y", out_dtype, (N, rows))
     need = jamba_moe_grouped_mx4_workspace_size(N, rows, cols, E)
     if need == 0:
         raise JmoeError(2, "jamba_moe_grouped_mx4_workspace_size")
     if workspace is None:
-        workspace = xq.new_empty(need)
-        made += [workspace]
+        workspace = _empty(xq, stream, (need,), torch.uint8, returned=False)
     else:
         _check(workspace, "workspace", torch.uint8)
     dev = _one_device(xq, xs=xs, offsets=offsets, Q=Q, S=S, y=y, workspace=workspace)
     st = _launch(lib.jamba_moe_grouped_mx4, dev, stream, xq.data_ptr(), xs.data_ptr(), offsets.data_ptr(), N, rows, cols,
                  E, Q.data_ptr(), S.data_ptr(), y.data_ptr(), OUT_BF16 if out_dtype == torch.bfloat16 else OUT_FP32,
                  workspace.data_ptr(), workspace.numel())
-    _made_here(stream, *made)
     if st != 0:
         raise JmoeError(st, "jamba_moe_grouped_mx4")
     return y
@@ -479,7 +482,6 @@ def jamba_moe_forward_mx4(x: torch.Tensor, router_W: torch.Tensor, router_bias: 
     S1, S3 uint8 [16][ffn][d / 32], Q2 uint8 [16][d][ffn / 2], S2 uint8 [16][d][ffn / 32] from
     jamba_moe_quantize_mx4.  Returns (y, topk_ids, topk_w)."""
     lib = load_library()
-    made = []  # what is allocated here
     _check(x, "x", torch.bfloat16)
     if x.dim() != 2:
         raise ValueError("x must be [T][d]")
@@ -496,26 +498,22 @@ def jamba_moe_forward_mx4(x: torch.Tensor, router_W: torch.Tensor, router_bias: 
     _check(S3, "S3", torch.uint8, (E, ffn, d // 32))
     _check(S2, "S2", torch.uint8, (E, d, ffn // 32))
     if y is None:
-        y = x.new_empty((T, d))
-        made += [y]
+        y = _empty(x, stream, (T, d), torch.bfloat16)
     else:
         _check(y, "y", torch.bfloat16, (T, d))
     if topk_ids is None:
-        topk_ids = x.new_empty((T, TOP_K), dtype=torch.int32)
-        made += [topk_ids]
+        topk_ids = _empty(x, stream, (T, TOP_K), torch.int32)
     else:
         _check(topk_ids, "topk_ids", torch.int32, (T, TOP_K))
     if topk_w is None:
-        topk_w = x.new_empty((T, TOP_K), dtype=torch.float32)
-        made += [topk_w]
+        topk_w = _empty(x, stream, (T, TOP_K), torch.float32)
     else:
         _check(topk_w, "topk_w", torch.float32, (T, TOP_K))
     need = jamba_moe_workspace_size_mx4(T, d, ffn, E, TOP_K)
     if need == 0:
         raise JmoeError(2, "jamba_moe_workspace_size_mx4")
     if workspace is None:
-        workspace = x.new_empty(need, dtype=torch.uint8)
-        made += [workspace]
+        workspace = _empty(x, stream, (need,), torch.uint8, returned=False)
     else:
         _check(workspace, "workspace", torch.uint8)
     p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
@@ -524,7 +522,6 @@ def jamba_moe_forward_mx4(x: torch.Tensor, router_W: torch.Tensor, router_bias: 
     st = _launch(lib.jamba_moe_forward_mx4, dev, stream, x.data_ptr(), router_W.data_ptr(), p(router_bias),
                  Q1.data_ptr(), S1.data_ptr(), Q3.data_ptr(), S3.data_ptr(), Q2.data_ptr(), S2.data_ptr(), T, d, ffn, E,
                  TOP_K, y.data_ptr(), topk_ids.data_ptr(), topk_w.data_ptr(), workspace.data_ptr(), workspace.numel())
-    _made_here(stream, *made)
     if st != 0:
         raise JmoeError(st, "jamba_moe_forward_mx4")
     return y, topk_ids, topk_w
