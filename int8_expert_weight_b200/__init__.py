@@ -5,8 +5,8 @@ the C ABI).  This module only marshals arguments: it checks dtypes, devices and 
 tensors, passes their device pointers and the current CUDA stream, and turns a non-zero status
 into a ``JmoeError``.  PyTorch provides device memory and streams; there is no CPU path.
 
-A call that is given a ``stream`` runs on it and nowhere else: its inputs have to be ready there, the MX4 calls
-allocate from that stream's pool, and another stream that reads the results has to wait for it.
+A call that is given a ``stream`` runs on it and nowhere else: its inputs have to be ready there, what it allocates
+comes from that stream's pool, and another stream that reads the results has to wait for it.
 
 Functions keep the C names: ``jamba_moe_quantize``, ``jamba_moe_workspace_size``,
 ``jamba_moe_forward`` (the ExpertsInt8 MoE layer), ``jamba_moe_forward_bf16w`` (unquantized bf16
@@ -213,8 +213,8 @@ def jamba_moe_quantize(W: torch.Tensor, stream: Optional[torch.cuda.Stream] = No
     rows, cols = W.shape[-2], W.shape[-1]
     n_mats = W.numel() // (rows * cols) if W.numel() else 0
     if out is None:
-        Q = torch.empty(W.shape, dtype=torch.int8, device=W.device)
-        S = torch.empty(W.shape[:-1], dtype=torch.float32, device=W.device)
+        Q = _empty(W, stream, W.shape, torch.int8)
+        S = _empty(W, stream, W.shape[:-1], torch.float32)
     else:
         Q, S = out
         _check(Q, "Q", torch.int8, W.shape)
@@ -258,13 +258,13 @@ def jamba_moe_forward(x: torch.Tensor, router_W: torch.Tensor, router_bias: Opti
     _check(S3, "S3", torch.float32, (E, ffn))
     _check(S2, "S2", torch.float32, (E, d))
     if y is None:
-        y = torch.empty((T, d), dtype=torch.bfloat16, device=x.device)
+        y = _empty(x, stream, (T, d), torch.bfloat16)
     _check(y, "y", torch.bfloat16, (T, d))
     if want_routing:
         if topk_ids is None:
-            topk_ids = torch.empty((T, TOP_K), dtype=torch.int32, device=x.device)
+            topk_ids = _empty(x, stream, (T, TOP_K), torch.int32)
         if topk_w is None:
-            topk_w = torch.empty((T, TOP_K), dtype=torch.float32, device=x.device)
+            topk_w = _empty(x, stream, (T, TOP_K), torch.float32)
     if topk_ids is not None:
         _check(topk_ids, "topk_ids", torch.int32, (T, TOP_K))
     if topk_w is not None:
@@ -273,7 +273,7 @@ def jamba_moe_forward(x: torch.Tensor, router_W: torch.Tensor, router_bias: Opti
     if need == 0:
         raise JmoeError(2, "jamba_moe_workspace_size")
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _empty(x, stream, (need,), torch.uint8, returned=False)
     _check(workspace, "workspace", torch.uint8)
     p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
     dev = _one_device(x, router_W=router_W, router_bias=router_bias, Q1=Q1, S1=S1, Q3=Q3, S3=S3, Q2=Q2, S2=S2, y=y,
@@ -299,8 +299,8 @@ def jamba_moe_quantize_fp8(W: torch.Tensor, stream: Optional[torch.cuda.Stream] 
     rows, cols = W.shape[-2], W.shape[-1]
     n_mats = W.numel() // (rows * cols) if W.numel() else 0
     if out is None:
-        Q = torch.empty(W.shape, dtype=torch.uint8, device=W.device)
-        S = torch.empty(W.shape[:-1], dtype=torch.float32, device=W.device)
+        Q = _empty(W, stream, W.shape, torch.uint8)
+        S = _empty(W, stream, W.shape[:-1], torch.float32)
     else:
         Q, S = out
         _check(Q, "Q", torch.uint8, W.shape)
@@ -343,19 +343,19 @@ def jamba_moe_forward_fp8(x: torch.Tensor, router_W: torch.Tensor, router_bias: 
     _check(S3, "S3", torch.float32, (E, ffn))
     _check(S2, "S2", torch.float32, (E, d))
     if y is None:
-        y = torch.empty((T, d), dtype=torch.bfloat16, device=x.device)
+        y = _empty(x, stream, (T, d), torch.bfloat16)
     _check(y, "y", torch.bfloat16, (T, d))
     if topk_ids is None:
-        topk_ids = torch.empty((T, TOP_K), dtype=torch.int32, device=x.device)
+        topk_ids = _empty(x, stream, (T, TOP_K), torch.int32)
     if topk_w is None:
-        topk_w = torch.empty((T, TOP_K), dtype=torch.float32, device=x.device)
+        topk_w = _empty(x, stream, (T, TOP_K), torch.float32)
     _check(topk_ids, "topk_ids", torch.int32, (T, TOP_K))
     _check(topk_w, "topk_w", torch.float32, (T, TOP_K))
     need = jamba_moe_workspace_size_fp8(T, d, ffn, E, TOP_K)
     if need == 0:
         raise JmoeError(2, "jamba_moe_workspace_size_fp8")
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _empty(x, stream, (need,), torch.uint8, returned=False)
     _check(workspace, "workspace", torch.uint8)
     p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
     dev = _one_device(x, router_W=router_W, router_bias=router_bias, Q1=Q1, S1=S1, Q3=Q3, S3=S3, Q2=Q2, S2=S2, y=y,
@@ -551,13 +551,13 @@ def jamba_mlp_forward(x: torch.Tensor, Q1: torch.Tensor, S1: torch.Tensor, Q3: t
     _check(S3, "S3", torch.float32, (ffn,))
     _check(S2, "S2", torch.float32, (d,))
     if y is None:
-        y = torch.empty((T, d), dtype=torch.bfloat16, device=x.device)
+        y = _empty(x, stream, (T, d), torch.bfloat16)
     _check(y, "y", torch.bfloat16, (T, d))
     need = jamba_mlp_workspace_size(T, d, ffn)
     if need == 0:
         raise JmoeError(2, "jamba_mlp_workspace_size")
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _empty(x, stream, (need,), torch.uint8, returned=False)
     _check(workspace, "workspace", torch.uint8)
     dev = _one_device(x, Q1=Q1, S1=S1, Q3=Q3, S3=S3, Q2=Q2, S2=S2, y=y, workspace=workspace)
     with torch.cuda.device(dev):
@@ -586,9 +586,9 @@ def jamba_moe_forward_bf16w(x: torch.Tensor, router_W: torch.Tensor, router_bias
     _check(W1, "W1", torch.bfloat16, (E, ffn, d))
     _check(W3, "W3", torch.bfloat16, (E, ffn, d))
     _check(W2, "W2", torch.bfloat16, (E, d, ffn))
-    y = torch.empty((T, d), dtype=torch.bfloat16, device=x.device) if y is None else y
-    topk_ids = torch.empty((T, TOP_K), dtype=torch.int32, device=x.device) if topk_ids is None else topk_ids
-    topk_w = torch.empty((T, TOP_K), dtype=torch.float32, device=x.device) if topk_w is None else topk_w
+    y = _empty(x, stream, (T, d), torch.bfloat16) if y is None else y
+    topk_ids = _empty(x, stream, (T, TOP_K), torch.int32) if topk_ids is None else topk_ids
+    topk_w = _empty(x, stream, (T, TOP_K), torch.float32) if topk_w is None else topk_w
     _check(y, "y", torch.bfloat16, (T, d))
     _check(topk_ids, "topk_ids", torch.int32, (T, TOP_K))
     _check(topk_w, "topk_w", torch.float32, (T, TOP_K))
@@ -596,7 +596,7 @@ def jamba_moe_forward_bf16w(x: torch.Tensor, router_W: torch.Tensor, router_bias
     if need == 0:
         raise JmoeError(2, "jamba_moe_workspace_size")
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _empty(x, stream, (need,), torch.uint8, returned=False)
     _check(workspace, "workspace", torch.uint8)
     p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
     dev = _one_device(x, router_W=router_W, router_bias=router_bias, W1=W1, W3=W3, W2=W2, y=y, topk_ids=topk_ids,
@@ -683,18 +683,18 @@ def jamba_moe_ep_dispatch(x: torch.Tensor, router_W: torch.Tensor, router_bias: 
     if router_bias is not None:
         _check(router_bias, "router_bias", torch.float32, (E,))
     dev = x.device
-    out = dict(send_x=torch.empty((T * TOP_K, d), dtype=torch.bfloat16, device=dev),
-               send_expert=torch.empty(T * TOP_K, dtype=torch.int32, device=dev),
-               send_w=torch.empty(T * TOP_K, dtype=torch.float32, device=dev),
-               send_counts=torch.empty(n_ranks, dtype=torch.int32, device=dev),
-               pos=torch.empty((T, TOP_K), dtype=torch.int32, device=dev),
-               topk_ids=torch.empty((T, TOP_K), dtype=torch.int32, device=dev),
-               topk_w=torch.empty((T, TOP_K), dtype=torch.float32, device=dev))
+    out = dict(send_x=_empty(x, stream, (T * TOP_K, d), torch.bfloat16),
+               send_expert=_empty(x, stream, (T * TOP_K,), torch.int32),
+               send_w=_empty(x, stream, (T * TOP_K,), torch.float32),
+               send_counts=_empty(x, stream, (n_ranks,), torch.int32),
+               pos=_empty(x, stream, (T, TOP_K), torch.int32),
+               topk_ids=_empty(x, stream, (T, TOP_K), torch.int32),
+               topk_w=_empty(x, stream, (T, TOP_K), torch.float32))
     need = int(lib.jamba_moe_ep_dispatch_workspace_size(T, d, E, TOP_K))
     if need == 0:
         raise JmoeError(2, "jamba_moe_ep_dispatch_workspace_size")
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _empty(x, stream, (need,), torch.uint8)
     _check(workspace, "workspace", torch.uint8)
     p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
     _one_device(x, router_W=router_W, router_bias=router_bias, workspace=workspace)
@@ -730,13 +730,13 @@ def jamba_moe_ep_experts(xr: torch.Tensor, expert: torch.Tensor, w: torch.Tensor
     _check(S3, "S3", torch.float32, (n_local, ffn))
     _check(S2, "S2", torch.float32, (n_local, d))
     if out is None:
-        out = torch.empty((N, d), dtype=torch.float32, device=xr.device)
+        out = _empty(xr, stream, (N, d), torch.float32)
     _check(out, "out", torch.float32, (N, d))
     need = int(lib.jamba_moe_ep_experts_workspace_size(N, d, ffn))
     if need == 0:
         raise JmoeError(2, "jamba_moe_ep_experts_workspace_size")
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=xr.device)
+        workspace = _empty(xr, stream, (need,), torch.uint8, returned=False)
     _check(workspace, "workspace", torch.uint8)
     dev = _one_device(xr, expert=expert, w=w, Q1=Q1, S1=S1, Q3=Q3, S3=S3, Q2=Q2, S2=S2, out=out, workspace=workspace)
     with torch.cuda.device(dev):
@@ -759,7 +759,7 @@ def jamba_moe_ep_combine(ret: torch.Tensor, pos: torch.Tensor, y: Optional[torch
     _check(ret, "ret", torch.float32, (T * TOP_K, d))
     _check(pos, "pos", torch.int32, (T, TOP_K))
     if y is None:
-        y = torch.empty((T, d), dtype=torch.bfloat16, device=ret.device)
+        y = _empty(ret, stream, (T, d), torch.bfloat16)
     _check(y, "y", torch.bfloat16, (T, d))
     dev = _one_device(ret, pos=pos, y=y)
     with torch.cuda.device(dev):

@@ -78,6 +78,16 @@ def mx4_weights():
     return [z(16, 256, 64), z(16, 256, 4), z(16, 256, 64), z(16, 256, 4), z(16, 128, 128), z(16, 128, 8)]
 
 
+def weights(dt, n=16):
+    f = torch.float32
+    return [z(n, 256, 128, dt=dt), z(n, 256, dt=f), z(n, 256, 128, dt=dt), z(n, 256, dt=f), z(n, 128, 256, dt=dt),
+            z(n, 128, dt=f)]
+
+
+def router():
+    return z(16, 128, dt=torch.float32)
+
+
 GROUPED = [z(5, 64), z(5, 4), z(4, dt=torch.int32), z(3, 40, 64), z(3, 40, 4)]
 CALLS = {
     "quantize_mx4": lambda s: jm.jamba_moe_quantize_mx4(x(), stream=s),
@@ -85,6 +95,16 @@ CALLS = {
     "grouped_mx4": lambda s: jm.jamba_moe_grouped_mx4(*GROUPED, stream=s),
     "forward_mx4": lambda s: jm.jamba_moe_forward_mx4(x(), z(16, 128, dt=torch.float32), None, *mx4_weights(),
                                                       stream=s),
+    "quantize": lambda s: jm.jamba_moe_quantize(x(), stream=s),
+    "quantize_fp8": lambda s: jm.jamba_moe_quantize_fp8(x(), stream=s),
+    "forward": lambda s: jm.jamba_moe_forward(x(), router(), None, *weights(torch.int8), stream=s),
+    "forward_fp8": lambda s: jm.jamba_moe_forward_fp8(x(), router(), None, *weights(torch.uint8), stream=s),
+    "forward_bf16w": lambda s: jm.jamba_moe_forward_bf16w(x(), router(), None, *weights(torch.bfloat16)[::2], stream=s),
+    "mlp_forward": lambda s: jm.jamba_mlp_forward(x(), *[t[0] for t in weights(torch.int8)], stream=s),
+    "ep_dispatch": lambda s: jm.jamba_moe_ep_dispatch(x(), router(), None, 2, stream=s),
+    "ep_experts": lambda s: jm.jamba_moe_ep_experts(x(), z(4, dt=torch.int32), z(4, dt=torch.float32),
+                                                    *weights(torch.int8, 8), stream=s),
+    "ep_combine": lambda s: jm.jamba_moe_ep_combine(z(8, 128, dt=torch.float32), z(4, 2, dt=torch.int32), stream=s),
 }
 
 
