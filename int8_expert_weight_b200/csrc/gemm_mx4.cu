@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
     const int KB = (KW + kWords - 1) / kWords;  // stages per tile; the last need not be whole
     int issued = 0;                    // codes: stages copied; MMA issuer: stages multiplied
     auto wait = [&](uint64_t* bar, int round) -> bool {
-        if (tc::mbar_wait_bounded(bar, round & 1, &abort_flag, p.max_polls)) return true;
+        if (tc::mbar_wait_bounded<kPair>(bar, round & 1, &abort_flag, p.max_polls)) return true;
         if (!abort_flag) fail(p.hdr, &abort_flag);
         return false;
     };
@@ -355,8 +355,10 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
     // in place of an elected lane: 570 instead of 425 us for the large product; only the issuing lane in the loop:
     // 485; a vote on each wait: 450.)
     const bool lead = tc::elect_one();
-    // Arrive on the barrier of the CTA that issues the MMAs.  What it then starts in this CTA (its tensor core reading
-    // this CTA's scales, or overwriting the accumulator) is ordered after this thread's own proxy or tcgen05 fence.
+    // Arrive on the barrier of the CTA that issues the MMAs.  Its copies and MMAs for the pair then read this CTA's
+    // scales, or overwrite its accumulator.  Scales: each lane's fence into the async proxy, the warp's barrier, release
+    // and acquire at cluster scope (kPair), the issuer's copies.  Accumulator: tcgen05 fences before the arrival and
+    // after the issuer's wait.
     auto arrive = [&](uint64_t* bar) {
         if constexpr (kPair)
             tc::mbar_arrive_cluster(tc::map_to_cta(tc::smem_u32(bar), 0));

@@ -37,21 +37,37 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t by
                  "r"(bytes)
                  : "memory");
 }
+// kCluster: relaxed, at cluster scope; mbar_wait_bounded's fence follows.
+template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
+    if constexpr (kCluster)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], "
+            "%2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, "
+            "p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
     return ok != 0;
 }
 // Wait for the phase with the given parity to complete, giving up after max_polls tries or when
-// *abort becomes non-zero.  Returns true when the phase completed.
+// *abort becomes non-zero.  Returns true when the phase completed.  kCluster: for a barrier that the other CTA of a
+// pair arrives on; acquires at cluster scope, see mbar_arrive_cluster.
+template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity, const volatile int* abort,
                                                   uint32_t max_polls) {
     for (uint32_t i = 0; i < max_polls; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (mbar_try_wait<kCluster>(bar, parity)) {
+            if constexpr (kCluster) asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+            return true;
+        }
         if (*abort) return false;
         if (i > 64) __nanosleep(64);
     }
@@ -73,11 +89,15 @@ __device__ __forceinline__ uint32_t map_to_cta(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-// Arrive on a barrier given by its cluster-window address.  Release at CTA scope: the other CTA learns that this
-// thread got here and reads none of its writes.  (At cluster scope each arrival waits for the thread's
-// accesses in flight.)
+// Arrive on a barrier given by its cluster-window address, with release at cluster scope of what was written to this
+// CTA's shared memory (by this thread, or by threads it has synchronised with): the instructions that the other CTA
+// issues for the pair after its wait (mbar_wait_bounded<true>: the matching acquire) read it.  Nothing else is handed
+// over this way: global memory and registers are not (a plain .release.cluster with .acquire.cluster waits for every
+// access in flight: 408 -> 660 us for 16384 x 14336 x 4096; as it is, 405), and reads of tensor memory are ordered
+// by tcgen05 fences.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // ------------------------------------------------------------------ TMA
