@@ -370,12 +370,18 @@ def jamba_moe_forward_fp8(x: torch.Tensor, router_W: torch.Tensor, router_bias: 
     return y, topk_ids, topk_w
 
 
+def _mx4_no_rows(numel: int, cols: int) -> bool:
+    """No rows of a width that the MX4 conversions take: the result is empty, and nothing is launched (the C calls want
+    a row at least)."""
+    return numel == 0 and cols % 32 == 0 and 32 <= cols <= 1 << 20
+
+
 def jamba_moe_quantize_mx4(W: torch.Tensor, stream: Optional[torch.cuda.Stream] = None,
                            out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None
                            ) -> Tuple[torch.Tensor, torch.Tensor]:
     """MX4 quantization of bf16 rows [..., rows, cols], cols a multiple of 32 (weights or activations).
     Returns (Q uint8 [..., rows, cols / 2], two E2M1 codes a byte, the even element low;
-    S uint8 [..., rows, cols / 32], one E8M0 scale per block of 32)."""
+    S uint8 [..., rows, cols / 32], one E8M0 scale per block of 32); empty ones for no rows."""
     lib = load_library()
     _check(W, "W", torch.bfloat16)
     if W.dim() < 2:
@@ -391,6 +397,8 @@ def jamba_moe_quantize_mx4(W: torch.Tensor, stream: Optional[torch.cuda.Stream] 
         _check(Q, "Q", torch.uint8, q_shape)
         _check(S, "S", torch.uint8, s_shape)
     dev = _one_device(W, Q=Q, S=S)
+    if _mx4_no_rows(W.numel(), cols):
+        return Q, S
     st = _launch(lib.jamba_moe_quantize_mx4, dev, stream, W.data_ptr(), n_mats, rows, cols, Q.data_ptr(), S.data_ptr())
     if st != 0:
         raise JmoeError(st, "jamba_moe_quantize_mx4")
@@ -400,7 +408,7 @@ def jamba_moe_quantize_mx4(W: torch.Tensor, stream: Optional[torch.cuda.Stream] 
 def jamba_moe_dequantize_mx4(Q: torch.Tensor, S: torch.Tensor, out: Optional[torch.Tensor] = None,
                              stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """The values of MX4 codes Q uint8 [..., rows, cols / 2] and scales S uint8 [..., rows, cols / 32]
-    as bf16 [..., rows, cols], exact."""
+    as bf16 [..., rows, cols], exact; empty for no rows."""
     lib = load_library()
     _check(Q, "Q", torch.uint8)
     if Q.dim() < 2:
@@ -414,6 +422,8 @@ def jamba_moe_dequantize_mx4(Q: torch.Tensor, S: torch.Tensor, out: Optional[tor
     else:
         _check(out, "out", torch.bfloat16, w_shape)
     dev = _one_device(Q, S=S, out=out)
+    if _mx4_no_rows(Q.numel(), cols):
+        return out
     st = _launch(lib.jamba_moe_dequantize_mx4, dev, stream, Q.data_ptr(), S.data_ptr(), n_mats, rows, cols,
                  out.data_ptr())
     if st != 0:
