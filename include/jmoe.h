@@ -35,7 +35,7 @@
  *     128 <= d, ffn <= 32768, 0 <= T <= 1048576.  Anything else returns JMOE_ERR_SHAPE.
  *   - T = 0 (no token) is valid for every forward call but jamba_moe_forward_noalloc: it returns
  *     JMOE_OK at once, after the size checks, without touching any pointer (they may be NULL) and
- *     without launching anything.
+ *     without launching anything; the status word of a workspace stays as it was.
  */
 #ifndef JMOE_H
 #define JMOE_H
@@ -222,7 +222,8 @@ int jamba_moe_dequantize_mx4(const uint8_t* Q, const uint8_t* S, int64_t n_mats,
  * Numerics: products exact, accumulated in fp32, rounded once to the output type; deterministic.
  * Sizes: 0 <= N <= 1<<20, 1 <= rows <= 65536, cols a multiple of 128 in [128, 32768], 1 <= n_experts <= 256
  * (not only the layer's 16: any model's experts, or one dense matrix); xq, Q, y 16-byte, xs, S, offsets 4-byte
- * aligned.  N = 0 returns at once.
+ * aligned.  N = 0 computes nothing: all pointers may be NULL; of a workspace that is given (256-byte aligned,
+ * large enough) the status word becomes JMOE_OK.
  */
 enum { JMOE_OUT_BF16 = 0, JMOE_OUT_FP32 = 1 };
 size_t jamba_moe_grouped_mx4_workspace_size(int64_t N, int64_t rows, int64_t cols, int n_experts);

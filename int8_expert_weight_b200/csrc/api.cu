@@ -964,7 +964,13 @@ int jamba_moe_grouped_mx4(const uint8_t* xq, const uint8_t* xs, const int32_t* o
                           void* workspace, size_t workspace_bytes, void* stream) {
     if (!grouped_shape_ok(N, rows, cols, n_experts)) return JMOE_ERR_SHAPE;
     if (out_type != JMOE_OUT_BF16 && out_type != JMOE_OUT_FP32) return JMOE_ERR_SHAPE;
-    if (N == 0) return JMOE_OK;
+    if (N == 0) {  // only the status word, if there is one: it is this call's, not the last one's
+        const bool usable = workspace && (reinterpret_cast<uintptr_t>(workspace) & 255) == 0 &&
+                            workspace_bytes >= kHeaderBytes;
+        if (!usable) return JMOE_OK;
+        return to_status(cudaMemsetAsync(&static_cast<WsHeader*>(workspace)->status, 0, sizeof(uint32_t),
+                                         static_cast<cudaStream_t>(stream)));
+    }
     if (!xq || !xs || !offsets || !Q || !S || !y || !workspace) return JMOE_ERR_NULL;
     const void* ptrs16[] = {xq, Q, y};
     for (const void* p : ptrs16)
