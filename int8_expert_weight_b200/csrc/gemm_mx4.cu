@@ -141,10 +141,6 @@ __device__ __forceinline__ void tile_at(const Groups& G, const Args& p, int L, T
     t.ntok = min(kTok, count - m * kTok);
 }
 
-// SiLU with the fast exponential and division intrinsics: a few fp32 ulps from the exact value,
-// far below the bf16 rounding of h that follows.
-__device__ __forceinline__ float silu_fast(float a) { return __fdividef(a, 1.0f + __expf(-a)); }
-
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
     uint4 q;
     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"

@@ -155,10 +155,6 @@ __device__ __forceinline__ bool tile_at(const WsHeader* hdr, const Args& p, int 
 __device__ __forceinline__ void tmem_st_n(uint32_t taddr, const uint32_t (&r)[8]) { tc::tmem_st8(taddr, r); }
 __device__ __forceinline__ void tmem_st_n(uint32_t taddr, const uint32_t (&r)[16]) { tc::tmem_st16(taddr, r); }
 
-// SiLU with the fast exponential and division intrinsics: a few fp32 ulps from the exact value,
-// far below the bf16 rounding of h that follows.
-__device__ __forceinline__ float silu_fast(float a) { return __fdividef(a, 1.0f + __expf(-a)); }
-
 __device__ __forceinline__ void fail(WsHeader* hdr, volatile int* abort) {
     *abort = 1;
     set_status(hdr, JMOE_DEV_TIMEOUT);
