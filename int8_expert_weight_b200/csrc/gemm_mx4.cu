@@ -47,12 +47,12 @@
 // few tiles divided evenly among all CTAs with partial sums through memory (two rows x 4096 x 14336: 18.7 -> 21.1 us,
 // the exchange costs what the balance gains), tiles of 64 weight rows (17.0 -> 19.0 us: the stages' pace, not their
 // bytes, bounds 64 CTAs), a look at the next stage's barrier between a stage's MMAs (414 -> 427 us).
-#include <cuda.h>
 
 #include <atomic>
 
 #include "mx4.cuh"
 #include "tc.cuh"
+#include "tmap.cuh"
 
 namespace jmoe {
 namespace ts {
@@ -660,34 +660,10 @@ __global__ void __launch_bounds__(Cfg<kPair, kTok>::kThreads, 1)
 }
 
 // ---------------------------------------------------------------- host side
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// Looked up once; the initialisation of a function-local static is thread-safe.
-EncodeTiledFn encode_fn() {
-    static const EncodeTiledFn fn = []() -> EncodeTiledFn {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            return reinterpret_cast<EncodeTiledFn>(f);
-        return nullptr;
-    }();
-    return fn;
-}
-
-// Codes [rows][K / 2], boxes of [box_rows][128 bytes]; what lies past the edges reads as zero.
-bool make_map(CUtensorMap* m, const uint8_t* ptr, uint64_t rows, uint64_t row_bytes, uint32_t box_rows) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[2] = {row_bytes, rows};
-    cuuint64_t strides[1] = {row_bytes};
-    cuuint32_t box[2] = {kSubBytes, box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(ptr), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+// Codes [rows][K / 2], boxes of [box_rows][128 bytes].
+bool codes_map(CUtensorMap* m, const uint8_t* ptr, uint64_t rows, uint64_t row_bytes, uint32_t box_rows) {
+    return make_map(m, ptr, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, row_bytes, box_rows, kSubBytes,
+                    CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <bool kDual, bool kPair, int kTok>
@@ -696,11 +672,11 @@ cudaError_t launch(Args p, cudaStream_t st, int num_sms) {
     CUtensorMap tx, txs, tw0, tw1;
     const uint64_t row_bytes = (uint64_t)p.K / 2, w_rows = (uint64_t)p.E * p.M;
     constexpr uint32_t kWBox = kDual ? 16 : kWRows;
-    if (!make_map(&tx, p.xq, (uint64_t)p.N, row_bytes, C::kTokCta) ||
-        !make_map(&txs, p.xq, (uint64_t)p.N, row_bytes, kBoxRows) || !make_map(&tw0, p.qa, w_rows, row_bytes, kWBox))
+    if (!codes_map(&tx, p.xq, (uint64_t)p.N, row_bytes, C::kTokCta) ||
+        !codes_map(&txs, p.xq, (uint64_t)p.N, row_bytes, kBoxRows) || !codes_map(&tw0, p.qa, w_rows, row_bytes, kWBox))
         return cudaErrorInvalidValue;
     tw1 = tw0;
-    if (kDual && !make_map(&tw1, p.qb, w_rows, row_bytes, kWBox)) return cudaErrorInvalidValue;
+    if (kDual && !codes_map(&tw1, p.qb, w_rows, row_bytes, kWBox)) return cudaErrorInvalidValue;
     const auto kernel = gemm_mx4_kernel<kDual, kPair, kTok>;
     static std::atomic<uint64_t> ready{0};  // devices whose kernel has its shared-memory limit raised
     int dev = 0;

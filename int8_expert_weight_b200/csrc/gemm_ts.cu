@@ -49,12 +49,12 @@
 // token operands of this path (x_perm from the gather kernel, h from the gemm13 epilogue) are stored
 // with elements 1 and 2 of every group of 4 swapped to match.  A k-permutation applied to both
 // operands leaves every dot product unchanged.
-#include <cuda.h>
 
 #include <atomic>
 
 #include "common.cuh"
 #include "tc.cuh"
+#include "tmap.cuh"
 
 namespace jmoe {
 namespace ts {
@@ -584,36 +584,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- host side
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// Looked up once; the initialisation of a function-local static is thread-safe.
-EncodeTiledFn encode_fn() {
-    static const EncodeTiledFn fn = []() -> EncodeTiledFn {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            return reinterpret_cast<EncodeTiledFn>(f);
-        return nullptr;
-    }();
-    return fn;
-}
-
-// 2D row-major [rows][cols] tensor, box [box_rows][box_cols].
-bool make_map(CUtensorMap* m, const void* ptr, CUtensorMapDataType dt, int elem_bytes, uint64_t rows, uint64_t cols,
-              uint32_t box_rows, uint32_t box_cols, CUtensorMapSwizzle sw) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[2] = {cols, rows};
-    cuuint64_t strides[1] = {cols * elem_bytes};
-    cuuint32_t box[2] = {box_cols, box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    return fn(m, dt, 2, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Token tiles per band: the band's activations (band * 256 rows * K bf16) near 48 MB of L2.
 int band_for(int64_t K) {
     const int64_t per_tile = (int64_t)kTokMax * K * 2;
