@@ -221,9 +221,11 @@ int jamba_moe_dequantize_mx4(const uint8_t* Q, const uint8_t* S, int64_t n_mats,
  *
  * Numerics: products exact, accumulated in fp32, rounded once to the output type; deterministic.
  * Sizes: 0 <= N <= 1<<20, 1 <= rows <= 65536, cols a multiple of 128 in [128, 32768], 1 <= n_experts <= 256
- * (not only the layer's 16: any model's experts, or one dense matrix); xq, Q, y 16-byte, xs, S, offsets 4-byte
- * aligned.  N = 0 computes nothing: all pointers may be NULL; of a workspace that is given (256-byte aligned,
- * large enough) the status word becomes JMOE_OK.
+ * (not only the layer's 16; one dense matrix is one expert); xq, Q, y 16-byte, xs, S, offsets 4-byte aligned.
+ * Other widths that jamba_moe_quantize_mx4 takes (multiples of 32) have to be padded before they are quantized, x and W
+ * with zeros up to a multiple of 128: blocks of zeros add nothing.
+ * N = 0 computes nothing: all pointers may be NULL; of a workspace that is given (256-byte aligned, large enough) the
+ * status word becomes JMOE_OK.
  */
 enum { JMOE_OUT_BF16 = 0, JMOE_OUT_FP32 = 1 };
 size_t jamba_moe_grouped_mx4_workspace_size(int64_t N, int64_t rows, int64_t cols, int n_experts);

@@ -86,6 +86,23 @@ def test_rows_of_no_expert_in_bf16(rows, scale):
     assert (got[:at[0]] == seven).all() and (got[at[3]:] == seven).all()
 
 
+@pytest.mark.parametrize("cols", [2880, 160, 32])
+def test_width_padded_with_zeros(cols):
+    """Rows of a width that the product refuses, padded with zeros before they are quantised."""
+    g = torch.Generator("cuda").manual_seed(cols)
+    x = torch.randint(-6, 7, (50, cols), generator=g, device="cuda").bfloat16()
+    w = torch.randint(-6, 7, (2, 40, cols), generator=g, device="cuda").bfloat16()
+    pad = -cols % 128
+    with pytest.raises(jm.JmoeError):
+        product(jm.jamba_moe_quantize_mx4(x), jm.jamba_moe_quantize_mx4(w), [0, 20, 50])
+    xp, wp = (jm.jamba_moe_quantize_mx4(torch.nn.functional.pad(t, (0, pad))) for t in (x, w))
+    y = product(xp, wp, [0, 20, 50])
+    # blocks' largest magnitudes are 1 to 6: scales 1/4 to 1, sums multiples of 2^-6 and below 36 * 2880
+    assert 36 * cols * 2 ** 6 <= 2 ** 24
+    want = ref.grouped(values(*jm.jamba_moe_quantize_mx4(x)), [0, 20, 50], values(*jm.jamba_moe_quantize_mx4(w)))[0]
+    assert np.array_equal(y.cpu().numpy(), want)
+
+
 # ------------------------------------------------------------------ the layer at the widths that models have
 def value_table(q, s):
     """fp64 values of one matrix on the device."""
