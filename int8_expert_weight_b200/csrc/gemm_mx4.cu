@@ -41,9 +41,11 @@
 // 4096: 535 MB for 534).
 //
 // Measured (random codes; B200, 6.46 TB/s copy, 1.71 PFLOP/s bf16): 128 rows over 16 experts, 14336 x 4096: 80 us,
-// 6.2 TB/s: HBM.  16384 rows: 425 us, 4.5 PFLOP/s, tensor pipe 71 % active; 320 us on constant codes (265 of them
-// without the epilogue, 245 without MMAs either: what the copies alone need), and 500 us back to back for seconds:
-// mostly the power limit, less the pipeline, sets the pace.  Tried and dropped: the stages of
+// 6.2 TB/s: HBM.  16384 rows: 421 us in short runs, 4.6 PFLOP/s, tensor pipe 70 % active; back to back for seconds 490 us
+// at the 1290 MHz that the power limit leaves, and on constant codes 356 us at 1762 MHz: 630 thousand cycles with either,
+// 321 us at the full 1965 MHz, where the operations need 282 at four times the bf16 rate.  (Constant codes in short runs:
+// 324 us; before the last changes 320, of which 265 without the epilogue and 245, the copies alone, without MMAs either.)
+// So the power limit sets the pace of long runs, and the pipeline is 14 % from its own.  Tried and dropped: the stages of
 // few tiles divided evenly among all CTAs with partial sums through memory (two rows x 4096 x 14336: 18.7 -> 21.1 us,
 // the exchange costs what the balance gains), tiles of 64 weight rows (17.0 -> 19.0 us: the stages' pace, not their
 // bytes, bounds 64 CTAs), a look at the next stage's barrier between a stage's MMAs (414 -> 427 us).
@@ -725,7 +727,9 @@ cudaError_t launch_grouped_mx4(const mx4::Args& p, cudaStream_t st, int num_sms)
     // Few rows per expert: single CTAs with narrow token tiles, whose stages are the weights in flight; else pairs.
     // Single or pairs, us, 14336 x 4096 weights of 16 experts, by rows of each: 4: 79 / 84, 48: 85 / 89, 64: 86 / 90,
     // 96: 104 / 94, 128: 120 / 97.  A group over 64 rows takes two narrow tiles, and uneven groups reach that at a mean
-    // of 48.
+    // of 48.  The host knows the mean alone, of all rows over all experts, so very uneven groups take the slower one:
+    // 12288 rows all in one of 256 experts, 4096 x 4096 weights, 157 / 88 (single is taken); 768 in one of 16, 14336 x
+    // 4096, 43 / 32 (single); 128 rows in groups of 8 and 16256 of no expert 82 / 86 (pairs).
     const bool few = p.rows <= (int64_t)48 * p.E;
     if (p.qb) return few ? launch<true, false, 64>(p, st, num_sms) : launch<true, true, 208>(p, st, num_sms);
     return few ? launch<false, false, 64>(p, st, num_sms) : launch<false, true, 208>(p, st, num_sms);
