@@ -44,7 +44,7 @@
 // 6.2 TB/s: HBM.  16384 rows: 421 us in short runs, 4.6 PFLOP/s, tensor pipe 70 % active; back to back for seconds 490 us
 // at the 1290 MHz that the power limit leaves, and on constant codes 356 us at 1762 MHz: 630 thousand cycles with either,
 // 321 us at the full 1965 MHz, where the operations need 282 at four times the bf16 rate.  (Constant codes in short runs:
-// 324 us; before the last changes 320, of which 265 without the epilogue and 245, the copies alone, without MMAs either.)
+// 324 us; an earlier build took 320, 265 of them without the epilogue and 245, the copies alone, without MMAs either.)
 // So the power limit sets the pace of long runs, and the pipeline is 14 % from its own.  Tried and dropped: the stages of
 // few tiles divided evenly among all CTAs with partial sums through memory (two rows x 4096 x 14336: 18.7 -> 21.1 us,
 // the exchange costs what the balance gains), tiles of 64 weight rows (17.0 -> 19.0 us: the stages' pace, not their
